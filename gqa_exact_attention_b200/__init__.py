@@ -341,3 +341,10 @@ def gqa_attn_fwd_fp8(q, k, v, q_scale, k_scale, v_scale, cache_seqlens=None, out
             out.data_ptr(), code, lse.data_ptr(), B, Sq, Sk, Hq, Hk, d, float(scale),
             int(bool(causal)), int(pack_gqa), int(num_splits), stream.cuda_stream))
     return out, lse
+
+
+# the serving operators (libgqa_serve.so); imported last: they use the names above
+from .serving import *  # noqa: E402,F401,F403
+from .serving import __all__ as _serving_all  # noqa: E402
+
+__all__ += _serving_all

@@ -1,4 +1,4 @@
-"""In-tree build of libgqa_attn.so (nvcc, sm_100a only)."""
+"""In-tree build of libgqa_attn.so and libgqa_serve.so (nvcc, sm_100a only)."""
 from __future__ import annotations
 
 import glob
@@ -9,6 +9,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libgqa_attn.so")
 CSRC = os.path.join(HERE, "csrc")
+SERVE_LIB = os.path.join(HERE, "libgqa_serve.so")
+SERVE_CSRC = os.path.join(HERE, "csrc_serve")
 INCLUDE = os.path.join(ROOT, "include")
 
 NVCC_FLAGS = [
@@ -20,28 +22,55 @@ NVCC_FLAGS = [
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+    return _sources(CSRC)
+
+
+def _sources(folder):
+    return sorted(glob.glob(os.path.join(folder, "*.cu")) + glob.glob(os.path.join(folder, "*.cpp")))
+
+
+def _headers(folder):
+    return [f for e in ("*.h", "*.cuh") for f in glob.glob(os.path.join(folder, e))]
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    return _older(LIB, sources() + _headers(CSRC))
+
+
+def serve_stale() -> bool:
+    # the serving kernels share the forward's device headers
+    return _older(SERVE_LIB, _sources(SERVE_CSRC) + _headers(SERVE_CSRC) + _headers(CSRC))
+
+
+def _older(lib, deps) -> bool:
+    if not os.path.exists(lib):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    t = os.path.getmtime(lib)
+    return any(os.path.getmtime(d) > t for d in deps + _headers(INCLUDE))
+
+
+def _compile(lib, folders, files, verbose):
+    cmd = ["nvcc", *NVCC_FLAGS, "-I", INCLUDE]
+    for f in folders:
+        cmd += ["-I", f]
+    if verbose:
+        cmd += ["-Xptxas", "-v"]
+    subprocess.run(cmd + ["-o", lib, *files, "-ldl"], check=True)
+    return lib
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if any source is newer than it; return its path."""
+    """Compile each library if any of its sources is newer than it; return the forward's path."""
+    build_serve(force, verbose)
     if not force and not _stale():
         return LIB
-    cmd = ["nvcc", *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC]
-    if verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += ["-o", LIB, *sources(), "-ldl"]
-    subprocess.run(cmd, check=True)
-    return LIB
+    return _compile(LIB, [CSRC], sources(), verbose)
+
+
+def build_serve(force: bool = False, verbose: bool = False) -> str:
+    if not force and not serve_stale():
+        return SERVE_LIB
+    return _compile(SERVE_LIB, [SERVE_CSRC, CSRC], _sources(SERVE_CSRC), verbose)
 
 
 if __name__ == "__main__":

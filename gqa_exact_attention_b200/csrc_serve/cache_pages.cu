@@ -1,0 +1,456 @@
+// The pages of a paged KV cache: gqa_cache_resize, gqa_cache_fork, gqa_cache_compact.
+//
+// Taking pages is a prefix problem: request i, which needs a_i pages, gets those free pages
+// (page_refs = 0) whose rank among the free ones, in order of their numbers, lies in
+// [a_0 + .. + a_{i-1}, a_0 + .. + a_i).  One cluster of 8 thread blocks does a whole call: it
+// validates the requests, gives up and shares pages, counts the free ones per warp, and each
+// warp then writes the ranks of its own pages into the table.  The steps are separated by
+// cluster barriers (a fraction of a microsecond) instead of launches, and the state stays in
+// L2, so a call costs about one launch.  Nothing depends on the order in which atomics land:
+// the counts only add up.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "gqa_serve.h"
+#include "launch_serve.h"
+
+namespace gqa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kClusterCtas = 8;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kEmpty = -1;
+
+__device__ __forceinline__ int pages_of(int len, int shift) { return (len >> shift) + ((len & ((1 << shift) - 1)) != 0); }
+__device__ __forceinline__ int clamp_len(int len, const CacheState& c) {
+    const long long cap = (long long)c.M << c.page_shift;
+    return len < 0 ? 0 : (len > cap ? (int)cap : len);
+}
+__device__ __forceinline__ bool known(int page, const CacheState& c) { return page >= 0 && page < c.P; }
+__device__ __forceinline__ int* row_of(const CacheState& c, int slot) { return c.table + (size_t)slot * c.M; }
+
+// Open-addressing set of slots in shared memory: the lowest request that names each.
+struct SlotSet {
+    int* keys;
+    int* first;
+    int mask;  // size - 1, a power of two of at least twice the requests
+    __device__ int place(int slot) const { return (int)(((unsigned)slot * 2654435761u) >> 7) & mask; }
+    __device__ void insert(int slot, int i) const {
+        for (int at = place(slot);; at = (at + 1) & mask) {
+            const int was = atomicCAS(&keys[at], kEmpty, slot);
+            if (was == kEmpty || was == slot) {
+                atomicMin(&first[at], i);
+                return;
+            }
+        }
+    }
+    // the lowest request that names the slot, or a value past every request
+    __device__ int find(int slot) const {
+        for (int at = place(slot);; at = (at + 1) & mask) {
+            if (keys[at] == slot) return first[at];
+            if (keys[at] == kEmpty) return 0x7fffffff;
+        }
+    }
+};
+
+__host__ __device__ constexpr int set_size(int n) {
+    int s = 64;
+    while (s < 2 * n) s *= 2;
+    return s;
+}
+
+// Inclusive prefix sum over a block's threads; *total is the block's sum.  64 bits: requests
+// may ask for more pages in all than 32 bits count.
+__device__ long long block_scan(long long x, long long* warp_sums, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    long long w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    const long long before = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    __syncthreads();
+    return incl + (warp == 0 ? 0 : before);
+}
+constexpr int kMost = 0x7fffffff;
+__device__ __forceinline__ int saturate(long long x) { return x > kMost ? kMost : (int)x; }
+
+template <bool FORK>
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
+    cache_plan_kernel(const __grid_constant__ PlanParams p) {
+    extern __shared__ int smem[];
+    __shared__ long long warp_sums[kWarps];
+    __shared__ int cta_free;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const CacheState& c = p.c;
+    const int n = p.n;
+    const int size = set_size(n);
+    int* upto = smem;       // [n] pages needed by requests 0..i
+    int* first = upto + n;  // [n] the first new entry of request i's row
+    int* old = first + n;   // [n] entries that request i gives up end here
+    int* state = old + n;   // [n] GQA_CACHE_DONE, _INVALID, _SHARED, or one of
+    constexpr int kSkip = 8;  // a fork of a slot to itself
+    constexpr int kTake = 9;  // as GQA_CACHE_DONE, if its pages can be had
+    auto acts = [&](int i) { return state[i] == GQA_CACHE_DONE || state[i] == kTake; };
+    const SlotSet keys{state + n, state + n + size, size - 1};
+    const SlotSet parents{state + n + 2 * size, state + n + 3 * size, size - 1};  // fork only
+
+    auto key_of = [&](int i) { return p.key != nullptr ? p.key[i] : i; };
+
+    // ---- 1. the requests, by every block alike (nothing of the state changes yet)
+    for (int i = tid; i < size; i += kThreads) {
+        keys.keys[i] = kEmpty;
+        keys.first[i] = 0x7fffffff;
+        if constexpr (FORK) {
+            parents.keys[i] = kEmpty;
+            parents.first[i] = 0x7fffffff;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+        const int key = key_of(i);
+        if (key >= 0 && key < c.S) keys.insert(key, i);
+        if constexpr (FORK) {
+            if (p.arg[i] >= 0 && p.arg[i] < c.S) parents.insert(p.arg[i], i);
+        }
+    }
+    __syncthreads();
+    long long carry = 0;
+    const int rounds = (n + kThreads - 1) / kThreads;
+    for (int r = 0; r < rounds; ++r) {
+        const int i = r * kThreads + tid;
+        int need = 0;
+        if (i < n) {
+            const int key = key_of(i), arg = p.arg[i];
+            int st = GQA_CACHE_INVALID, at = 0, end = 0;
+            if (key >= 0 && key < c.S && keys.find(key) == i) {
+                const int mine = clamp_len(c.lens[key], c);
+                if constexpr (FORK) {
+                    if (arg == key) {
+                        st = kSkip;
+                    } else if (arg >= 0 && arg < c.S && parents.find(key) > n) {
+                        const int len = clamp_len(c.lens[arg], c);
+                        st = GQA_CACHE_DONE;
+                        at = len >> c.page_shift;  // whole pages are shared
+                        end = pages_of(mine, c.page_shift);
+                        need = pages_of(len, c.page_shift) - at;
+                    }
+                } else if (arg >= 0 && arg <= ((long long)c.M << c.page_shift)) {
+                    st = GQA_CACHE_DONE;
+                    const int stay = min(mine, arg);
+                    if (arg != mine && (stay & ((1 << c.page_shift) - 1)) != 0) {
+                        const int page = row_of(c, key)[stay >> c.page_shift];
+                        if (known(page, c) && __ldcg(c.refs + page) > 1) st = GQA_CACHE_SHARED;
+                    }
+                    if (st == GQA_CACHE_DONE) {
+                        const int had = pages_of(mine, c.page_shift), want = pages_of(arg, c.page_shift);
+                        need = max(want - had, 0);
+                        at = need > 0 ? had : want;  // taken from here, or given up from here
+                        end = had;
+                    }
+                }
+            }
+            state[i] = need > 0 ? kTake : st;
+            first[i] = at;
+            old[i] = end;
+        }
+        long long total;
+        const long long incl = carry + block_scan(need, warp_sums, &total);
+        if (i < n) upto[i] = saturate(incl);
+        carry += total;
+    }
+    const int needed = saturate(carry);
+    cluster.sync();  // every block has read the state
+
+    // ---- 2. pages given up, and with FORK the shared ones named; 256 entries per warp and turn
+    constexpr int kChunk = 256;
+    const int chunks = (c.M + kChunk - 1) / kChunk;
+    const long long items = (long long)n * chunks;
+    for (long long w = (long long)rank * kWarps + warp; w < items; w += kClusterCtas * kWarps) {
+        const int i = (int)(w % n), j0 = (int)(w / n) * kChunk;
+        if (!acts(i)) continue;
+        const int lo = FORK ? 0 : first[i];
+        const int hi = FORK ? max(first[i], old[i]) : old[i];
+        if (j0 >= hi || j0 + kChunk <= lo) continue;
+        int* row = row_of(c, key_of(i));
+        const int* from = FORK ? row_of(c, p.arg[i]) : nullptr;
+        int was[kChunk / 32], now[kChunk / 32];
+#pragma unroll
+        for (int e = 0; e < kChunk / 32; ++e) {
+            const int j = j0 + e * 32 + lane;
+            was[e] = (j >= lo && j < old[i]) ? row[j] : -1;
+            now[e] = (FORK && j < first[i]) ? from[j] : -1;
+        }
+#pragma unroll
+        for (int e = 0; e < kChunk / 32; ++e) {
+            const int j = j0 + e * 32 + lane;
+            if (known(was[e], c)) atomicSub(c.refs + was[e], 1);
+            if (known(now[e], c)) atomicAdd(c.refs + now[e], 1);
+            if (j >= lo && j < hi) row[j] = now[e];
+        }
+    }
+
+    // ---- 3. the free pages, counted per warp over its own range of page numbers
+    int free_before = 0, free_all = 0;
+    const int per_warp = ((c.P + kClusterCtas * kWarps - 1) / (kClusterCtas * kWarps) + 31) / 32 * 32;
+    const long long p0 = (long long)(rank * kWarps + warp) * per_warp;
+    const int p_lo = p0 < c.P ? (int)p0 : c.P;
+    const int p_hi = p0 + per_warp < c.P ? (int)(p0 + per_warp) : c.P;
+    if (needed > 0) {
+        cluster.sync();  // the counts are final
+        int mine = 0;
+        for (int at = p_lo; at < p_hi; at += 32) {
+            const int page = at + lane;
+            mine += __popc(__ballot_sync(0xffffffffu, page < p_hi && __ldcg(c.refs + page) == 0));
+        }
+        long long total;
+        const int incl = (int)block_scan(lane == 31 ? mine : 0, warp_sums, &total);
+        // (lane 31 of each warp holds the sum up to and with its warp)
+        free_before = __shfl_sync(0xffffffffu, incl, 31) - mine;
+        if (tid == 0) cta_free = (int)total;
+        cluster.sync();
+        for (int r = 0; r < kClusterCtas; ++r) {
+            const int x = *cluster.map_shared_rank(&cta_free, r);
+            if (r < rank) free_before += x;
+            free_all += x;
+        }
+
+        // ---- 4. each warp hands out its own free pages
+        for (int at = p_lo; at < p_hi && free_before < needed; at += 32) {
+            const int page = at + lane;
+            const bool is_free = page < p_hi && __ldcg(c.refs + page) == 0;
+            const unsigned ball = __ballot_sync(0xffffffffu, is_free);
+            const int r = free_before + __popc(ball & ((1u << lane) - 1u));
+            free_before += __popc(ball);
+            if (is_free && r < needed) {
+                int lo = 0, hi = n - 1;  // the first request with upto > r
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (upto[mid] > r) hi = mid;
+                    else lo = mid + 1;
+                }
+                if (upto[lo] <= free_all) {
+                    const int before = lo > 0 ? upto[lo - 1] : 0;
+                    row_of(c, key_of(lo))[first[lo] + (r - before)] = page;
+                    c.refs[page] = 1;
+                }
+            }
+        }
+    }
+
+    // ---- 5. lengths and outcomes
+    for (int i = rank * kThreads + tid; i < n; i += kClusterCtas * kThreads) {
+        int st = state[i];
+        if (st == kTake) st = upto[i] <= free_all ? GQA_CACHE_DONE : GQA_CACHE_NO_PAGES;
+        if constexpr (FORK) {
+            if (acts(i))
+                c.lens[p.key[i]] = st == GQA_CACHE_DONE ? clamp_len(c.lens[p.arg[i]], c) : 0;
+        } else {
+            if (st == GQA_CACHE_DONE) c.lens[key_of(i)] = p.arg[i];
+        }
+        p.status[i] = st == kSkip ? (int)GQA_CACHE_DONE : st;
+    }
+    if constexpr (FORK) {
+        // a child without a page for its last rows gives the shared ones back
+        if (needed > free_all) {
+            cluster.sync();  // no warp looks for free pages any more
+            for (int i = rank * kWarps + warp; i < n; i += kClusterCtas * kWarps) {
+                if (state[i] != kTake || upto[i] <= free_all) continue;
+                int* row = row_of(c, p.key[i]);
+                for (int j = lane; j < first[i]; j += 32) {
+                    if (known(row[j], c)) atomicSub(c.refs + row[j], 1);
+                    row[j] = -1;
+                }
+            }
+        }
+    }
+    if (needed > 0) cluster.sync();  // a block's count is read by the others until here
+}
+
+// The last rows of each fork: [0, len % page) of the parent's last page to the child's, in
+// every layer's K and V.  A unit is 16 KB of one page; units past a fork's rows end at once.
+constexpr int kCopyBytes = 16384;
+constexpr int kCopyThreads = 256;
+
+__global__ void __launch_bounds__(kCopyThreads) cache_tail_copy_kernel(const __grid_constant__ PlanParams p,
+                                                                       const __grid_constant__ Pools pools,
+                                                                       int parts) {
+    const CacheState& c = p.c;
+    const long long units = (long long)p.n * pools.layers * 2 * parts;
+    const long long page_bytes = pools.row_bytes << c.page_shift;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int part = (int)(u % parts);
+        const int kv = (int)(u / parts % 2);
+        const int layer = (int)(u / (2ll * parts) % pools.layers);
+        const int i = (int)(u / (2ll * parts * pools.layers));
+        if (p.status[i] != GQA_CACHE_DONE || p.arg[i] == p.key[i]) continue;
+        const int len = clamp_len(c.lens[p.key[i]], c);
+        const int tail = len & ((1 << c.page_shift) - 1);
+        const long long bytes = tail * pools.row_bytes;
+        if ((long long)part * kCopyBytes >= bytes) continue;
+        const int entry = len >> c.page_shift;
+        const int src = row_of(c, p.arg[i])[entry], dst = row_of(c, p.key[i])[entry];
+        if (!known(src, c) || !known(dst, c)) continue;
+        uint8_t* pool = pools.kv[kv] + (size_t)layer * c.P * page_bytes;
+        const uint8_t* from = pool + (size_t)src * page_bytes;
+        uint8_t* to = pool + (size_t)dst * page_bytes;
+#pragma unroll
+        for (int e = 0; e < kCopyBytes / (16 * kCopyThreads); ++e) {
+            const long long at = (long long)part * kCopyBytes + (e * kCopyThreads + threadIdx.x) * 16;
+            if (at < bytes)
+                *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+        }
+    }
+}
+
+// What gqa_cache_compact does to one slot, decided from the state before the call.
+struct CompactSlot {
+    int len, base, end;  // old length, context, new length
+    int status;
+};
+__device__ CompactSlot compact_slot(const CompactParams& p, int s) {
+    // called by a whole block; the same answer for every thread
+    const CacheState& c = p.c;
+    CompactSlot r;
+    r.len = clamp_len(c.lens[s], c);
+    const int nodes = min(max(p.tree_lens != nullptr ? p.tree_lens[s] : p.T, 0), min(p.T, r.len));
+    const int m = p.keep_lens[s];
+    r.base = r.len - nodes;
+    r.end = r.base + m;
+    bool bad = m < 0 || m > nodes;
+    const int* keep = p.keep + (size_t)s * p.T;
+    if (!bad) {
+        for (int j = threadIdx.x; j < m; j += blockDim.x)
+            bad |= keep[j] <= (j > 0 ? keep[j - 1] : -1) || keep[j] >= nodes;
+    }
+    bad = __syncthreads_or(bad);
+    bool shared = false;
+    if (!bad) {
+        const int lo = r.base >> c.page_shift, hi = pages_of(r.end, c.page_shift);
+        for (int j = lo + threadIdx.x; j < hi; j += blockDim.x) {
+            const int page = row_of(c, s)[j];
+            shared |= known(page, c) && __ldcg(c.refs + page) > 1;
+        }
+    }
+    shared = __syncthreads_or(shared);
+    r.status = bad ? GQA_CACHE_INVALID : (shared ? GQA_CACHE_SHARED : GQA_CACHE_DONE);
+    return r;
+}
+
+// Moves the accepted rows.  A thread owns one 16-byte column of one layer's K or V and walks
+// the accepted nodes in order: node keep[j] >= j goes to place j, so a row is overwritten only
+// after it was read, and eight rows may be read before their eight writes.
+constexpr int kMoveThreads = 128;
+constexpr int kMoveBatch = 8;
+__global__ void __launch_bounds__(kMoveThreads) cache_compact_rows_kernel(const __grid_constant__ CompactParams p) {
+    const CacheState& c = p.c;
+    const int s = blockIdx.x;
+    const CompactSlot r = compact_slot(p, s);
+    if (blockIdx.y == 0 && threadIdx.x == 0) p.status[s] = r.status;
+    if (r.status != GQA_CACHE_DONE) return;
+    const int cols = (int)(p.pools.row_bytes / 16);
+    const long long item = (long long)blockIdx.y * kMoveThreads + threadIdx.x;
+    if (item >= 2ll * p.pools.layers * cols) return;
+    const int col = (int)(item % cols);
+    const int kv = (int)(item / cols % 2), layer = (int)(item / cols / 2);
+    uint8_t* pool = p.pools.kv[kv] + ((size_t)layer * c.P << c.page_shift) * p.pools.row_bytes + (size_t)col * 16;
+    const int* row = row_of(c, s);
+    const int* keep = p.keep + (size_t)s * p.T;
+    const int in_page = (1 << c.page_shift) - 1;
+    auto at = [&](int pos) -> uint8_t* {
+        const int page = row[pos >> c.page_shift];
+        if (!known(page, c)) return nullptr;
+        return pool + (((size_t)page << c.page_shift) + (pos & in_page)) * p.pools.row_bytes;
+    };
+    const int m = r.end - r.base;
+    for (int j0 = 0; j0 < m; j0 += kMoveBatch) {
+        uint4 x[kMoveBatch];
+        uint8_t* to[kMoveBatch];
+#pragma unroll
+        for (int e = 0; e < kMoveBatch; ++e) {
+            to[e] = nullptr;
+            const int j = j0 + e;
+            if (j < m && keep[j] > j) {
+                const uint8_t* from = at(r.base + keep[j]);
+                if (from != nullptr) {
+                    to[e] = at(r.base + j);
+                    x[e] = *reinterpret_cast<const uint4*>(from);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kMoveBatch; ++e)
+            if (to[e] != nullptr) *reinterpret_cast<uint4*>(to[e]) = x[e];
+    }
+}
+
+// The lengths and pages after the rows have moved: one warp per slot (a tree spans few pages).
+__global__ void __launch_bounds__(128) cache_compact_pages_kernel(const __grid_constant__ CompactParams p) {
+    const CacheState& c = p.c;
+    const int s = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (s >= c.S || p.status[s] != GQA_CACHE_DONE) return;
+    const int len = clamp_len(c.lens[s], c);
+    const int nodes = min(max(p.tree_lens != nullptr ? p.tree_lens[s] : p.T, 0), min(p.T, len));
+    const int end = len - nodes + p.keep_lens[s];
+    __syncwarp();
+    int* row = row_of(c, s);
+    for (int j = pages_of(end, c.page_shift) + lane; j < pages_of(len, c.page_shift); j += 32) {
+        if (known(row[j], c)) atomicSub(c.refs + row[j], 1);
+        row[j] = -1;
+    }
+    if (lane == 0) c.lens[s] = end;
+}
+
+template <bool FORK>
+cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
+    const size_t bytes = sizeof(int) * (4 * (size_t)p.n + (FORK ? 4 : 2) * (size_t)set_size(p.n));
+    if (bytes > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)bytes);
+        if (e != cudaSuccess) return e;
+    }
+    cache_plan_kernel<FORK><<<kClusterCtas, kThreads, bytes, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_resize(const PlanParams& p, cudaStream_t stream) { return launch_plan<false>(p, stream); }
+
+cudaError_t launch_fork(const PlanParams& p, const Pools& pools, int sms, cudaStream_t stream) {
+    cudaError_t e = launch_plan<true>(p, stream);
+    if (e != cudaSuccess) return e;
+    const long long page_bytes = pools.row_bytes << p.c.page_shift;
+    const int parts = (int)((page_bytes + kCopyBytes - 1) / kCopyBytes);
+    const long long units = (long long)p.n * pools.layers * 2 * parts;
+    const long long most = (long long)sms * 8;
+    cache_tail_copy_kernel<<<(unsigned)(units < most ? units : most), kCopyThreads, 0, stream>>>(p, pools, parts);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+    const long long items = 2ll * p.pools.layers * (p.pools.row_bytes / 16);
+    const dim3 grid((unsigned)p.c.S, (unsigned)((items + kMoveThreads - 1) / kMoveThreads));
+    cache_compact_rows_kernel<<<grid, kMoveThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cache_compact_pages_kernel<<<(p.c.S + 3) / 4, 128, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace gqa
