@@ -47,31 +47,15 @@ cudaError_t launch_fork(const PlanParams& p, const Pools& pools, int sms, cudaSt
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention
-struct AttnParams {
-    const uint16_t* q;
-    const uint16_t* k;
-    const uint16_t* v;
-    long long q_stride, k_stride, v_stride;  // elements between rows
-    void* out;
-    bool out_bf16;
-    float* lse;
-    int B, Hq, Hk, d;
-    float scale;
-    // packed prompts
-    const int* cu_q;
-    const int* cu_k;
-    int total_q, total_k;
-    int causal;
-    // tree over a cache
-    const int* table;  // NULL: dense [B, Sk, Hk, d]
-    int M, P, page_shift, Sk;
-    const int* seqlens;
-    const int* tree_lens;
-    const int* mask;
-    long long mask_stride;  // words between sequences (0: shared)
-    int T, W;
-};
-cudaError_t launch_attn_varlen(const AttnParams& p, cudaStream_t stream);
-cudaError_t launch_attn_tree(const AttnParams& p, cudaStream_t stream);
+struct ServeParams;
+struct ServePlanParams;
+
+int serve_ctas_per_sm(int nt);
+// The attention kernel for head dimension d and nt tiles per unit: packed prompts (seqlens NULL;
+// with a list, else by ranges and nt = 1) or a tree over a cache.
+cudaError_t launch_serve(const ServeParams& p, int d, int nt, int grid, cudaStream_t stream);
+cudaError_t launch_serve_list(const ServePlanParams& p, cudaStream_t stream);
+// Device address of this library's status word on the current device (NULL on error).
+unsigned int* serve_status_symbol();
 
 }  // namespace gqa

@@ -1,14 +1,17 @@
-// C ABI of libgqa_serve.so: argument validation and launches.  See include/gqa_serve.h for
-// the contract.
+// C ABI of libgqa_serve.so: argument validation, schedules, TMA tensor maps, scratch and
+// launches.  See include/gqa_serve.h for the contract.
 #include "gqa_serve.h"
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include "launch_serve.h"
+#include "serve_params.h"
 
 namespace {
 
@@ -66,9 +69,9 @@ int log2_of(int x) {
     return s;
 }
 
-// What both attention calls check of heads, head dimension, scale, output and splits.
-gqa_status check_heads(int Hq, int Hk, int d, float scale, int out_dtype, int num_splits) {
-    if (Hq < 1 || Hk < 1 || num_splits < 0) return GQA_ERR_SHAPE;
+// What both attention calls check of heads, head dimension, scale and output.
+gqa_status check_heads(int Hq, int Hk, int d, float scale, int out_dtype) {
+    if (Hq < 1 || Hk < 1) return GQA_ERR_SHAPE;
     if (out_dtype != GQA_OUT_F32 && out_dtype != GQA_OUT_BF16) return GQA_ERR_SHAPE;
     if (Hq % Hk != 0) return GQA_ERR_HEADS;
     if (d != 64 && d != 128) return GQA_ERR_HEADDIM;
@@ -127,6 +130,199 @@ gqa::Pools pools_of(void* k, void* v, int layers, long long row_bytes) {
     return p;
 }
 
+// ---------------------------------------------------------------- tensor maps, scratch, waits
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled get_encode_tiled() {
+    static EncodeTiled fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(ptr);
+    });
+    return fn;
+}
+
+// [B, S, H, d] as a 4-D map (d, H, S, B) with 128-byte swizzle, boxes of one row's 128 bytes x
+// box_h heads x box_s rows, zero fill out of bounds.  Rows lie row_bytes apart; fp32 tensors are
+// outputs, the others bf16.
+bool encode(CUtensorMap* m, const void* ptr, long long B, long long S, int H, int d, long long row_bytes,
+            int box_h, int box_s, bool f32 = false) {
+    EncodeTiled enc = get_encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t es = f32 ? 4 : 2;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)B};
+    // (one batch: its stride is never used, and the packed rows' total may exceed its limit)
+    cuuint64_t strides[3] = {(cuuint64_t)d * es, (cuuint64_t)row_bytes, (cuuint64_t)row_bytes * (B > 1 ? S : 1)};
+    cuuint32_t box[4] = {(cuuint32_t)(128 / es), (cuuint32_t)box_h, (cuuint32_t)box_s, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+               const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, f32 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scratch comes from a stream-ordered pool of this library per device, which keeps what is
+// freed.  In a stream capture an allocation becomes the graph's own.
+cudaMemPool_t workspace_pool(int dev) {
+    static cudaMemPool_t pools[64] = {};
+    static std::mutex mu;
+    if (dev < 0 || dev >= 64) return nullptr;
+    std::lock_guard<std::mutex> lk(mu);
+    if (pools[dev] == nullptr) {
+        cudaMemPoolProps props{};
+        props.allocType = cudaMemAllocationTypePinned;
+        props.location.type = cudaMemLocationTypeDevice;
+        props.location.id = dev;
+        cudaMemPool_t pool = nullptr;
+        if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        uint64_t keep = ~0ull;
+        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        pools[dev] = pool;
+    }
+    return pools[dev];
+}
+
+// One allocation on a stream, freed on it when the object goes (after the launches in between).
+class Workspace {
+public:
+    Workspace(int dev, size_t bytes, cudaStream_t stream) : stream_(stream) {
+        cudaMemPool_t pool = workspace_pool(dev);
+        if (pool == nullptr || std::getenv("GQA_FAULT_INJECT_ALLOC") != nullptr) return;
+        if (cudaMallocFromPoolAsync(&ptr_, bytes, pool, stream) != cudaSuccess) {
+            cudaGetLastError();
+            ptr_ = nullptr;
+        }
+    }
+    ~Workspace() {
+        if (ptr_ != nullptr) cudaFreeAsync(ptr_, stream_);
+    }
+    Workspace(const Workspace&) = delete;
+    Workspace& operator=(const Workspace&) = delete;
+    bool ok() const { return ptr_ != nullptr; }
+    // the next piece of the allocation, 256-byte aligned
+    template <class T>
+    T* take(size_t count) {
+        T* p = reinterpret_cast<T*>(static_cast<char*>(ptr_) + used_);
+        used_ += size_of<T>(count);
+        return p;
+    }
+    template <class T>
+    static size_t size_of(size_t count) {
+        return (count * sizeof(T) + 255) & ~(size_t)255;
+    }
+
+private:
+    void* ptr_ = nullptr;
+    size_t used_ = 0;
+    cudaStream_t stream_;
+};
+
+// Limit of each in-kernel wait, as gqa_attn_fwd reads it.
+long long timeout_ns() {
+    if (const char* e = std::getenv("GQA_WAIT_TIMEOUT_NS")) {
+        const long long ns = std::atoll(e);
+        return ns < 1 ? 1 : ns;
+    }
+    const char* e = std::getenv("GQA_WAIT_TIMEOUT_MS");
+    const long long ms = e ? std::atoll(e) : 4000;
+    return (ms < 1 ? 1 : ms) * 1000000ll;
+}
+
+// ---------------------------------------------------------------- attention schedules
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Heads, rows and waits: what does not depend on where K and V lie.  `queries` is the query rows
+// of a sequence (the average one's, for prompts): a tile holds a group's heads side by side
+// unless that pads more rows than a tile per head does.
+void fill_common(gqa::ServeParams* p, int B, int Hq, int Hk, float scale, long long queries) {
+    const int g = Hq / Hk, M = gqa::kServeBlockM;
+    p->B = B;
+    p->Hq = Hq;
+    p->Hk = Hk;
+    p->g = g;
+    const long long apart = (long long)g * ceil_div(queries, M);
+    p->pack = g <= M && ceil_div(queries, M / g) <= apart ? 1 : 0;
+    p->pos_per_tile = p->pack ? M / g : M;
+    p->rows_valid = p->pack ? g * p->pos_per_tile : M;
+    p->n_hg = p->pack ? Hk : Hq;
+    p->div_g = gqa::make_fastdiv((uint32_t)g);
+    p->div_hg = gqa::make_fastdiv((uint32_t)p->n_hg);
+    p->scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p->timeout_ns = timeout_ns();
+    p->drain_ns = p->timeout_ns > 1000000000ll ? p->timeout_ns : 1000000000ll;
+    // host-side fault injection: the kernel stalls on a wait that nothing completes
+    p->inject_stall = std::getenv("GQA_FAULT_INJECT_STALL") != nullptr ? 1 : 0;
+}
+
+// The ranges schedule: every CTA slot gets an equal share of all key blocks.
+gqa_status run_ranges(gqa::ServeParams* p, int dev, int sms, int d, int nt, cudaStream_t stream) {
+    const int grid = sms * gqa::serve_ctas_per_sm(nt);
+    const size_t rows = (size_t)2 * grid * nt * gqa::kServeBlockM;
+    const bool prefix = p->B > gqa::kServeOwnPrefix;
+    using W = Workspace;
+    W ws(dev, W::size_of<float>(rows * d) + W::size_of<float>(rows) + W::size_of<int>(2 * grid) +
+                  (prefix ? W::size_of<long long>((size_t)p->B + 1) : 0), stream);
+    if (!ws.ok()) return GQA_ERR_ALLOC;
+    p->part_o = ws.take<float>(rows * d);
+    p->part_lse = ws.take<float>(rows);
+    p->part_count = ws.take<int>(2 * grid);
+    p->pre = prefix ? ws.take<long long>((size_t)p->B + 1) : nullptr;
+    p->min_blocks = 2;
+    if (cudaMemsetAsync(p->part_count, 0, 2 * grid * sizeof(int), stream) != cudaSuccess) {
+        cudaGetLastError();
+        return GQA_ERR_CUDA;
+    }
+    return launched(gqa::launch_serve(*p, d, nt, grid, stream));
+}
+
+// The list schedule (two-tile units of prompts).
+gqa_status run_list(gqa::ServeParams* p, int dev, int sms, int d, cudaStream_t stream) {
+    gqa::ServePlanParams l{};
+    l.cu_q = p->cu_q;
+    l.cu_k = p->cu_k;
+    l.B = p->B;
+    l.total_q = p->total_q;
+    l.total_k = p->total_k;
+    l.causal = p->causal;
+    l.pos_per_unit = 2 * p->pos_per_tile;
+    // windows of about 12 MB of K and V (the forward's, fitted on B200: the L2 also carries Q and
+    // the output), at most kServeWindows of them
+    const long long rows = 12000000ll / (4ll * p->Hk * d);
+    long long window = rows > 1 ? rows : 1;
+    const long long least = ceil_div(p->total_k > 0 ? p->total_k : 1, gqa::kServeWindows);
+    if (window < least) window = least;
+    l.window_rows = (int)window;
+    l.windows = gqa::kServeWindows;
+    const long long cap = ceil_div(p->total_q, l.pos_per_unit) + p->B;
+    l.list_cap = (int)cap;
+    using W = Workspace;
+    W ws(dev, W::size_of<int2>((size_t)cap) + W::size_of<int>(1), stream);
+    if (!ws.ok()) return GQA_ERR_ALLOC;
+    l.list = ws.take<int2>((size_t)cap);
+    l.list_len = ws.take<int>(1);
+    p->list = l.list;
+    p->list_len = l.list_len;
+    p->kv_shared = 1;
+    if (gqa::launch_serve_list(l, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return GQA_ERR_CUDA;
+    }
+    const long long units = cap * p->n_hg;
+    return launched(gqa::launch_serve(*p, d, 2, (int)(units < sms ? units : sms), stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -135,10 +331,9 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
                                long long k_row_stride, const void* v, long long v_row_stride,
                                const int* cu_seqlens_q, const int* cu_seqlens_k, void* out,
                                int out_dtype, float* lse, int B, int total_q, int total_k, int Hq,
-                               int Hk, int d, float scale, int causal, int num_splits,
-                               void* stream) {
+                               int Hk, int d, float scale, int causal, void* stream) {
     if (B < 1 || total_q < 0 || total_k < 0) return GQA_ERR_SHAPE;
-    gqa_status st = check_heads(Hq, Hk, d, scale, out_dtype, num_splits);
+    gqa_status st = check_heads(Hq, Hk, d, scale, out_dtype);
     if (st != GQA_OK) return st;
     if (!stride_ok(&q_row_stride, (long long)Hq * d) || !stride_ok(&k_row_stride, (long long)Hk * d) ||
         !stride_ok(&v_row_stride, (long long)Hk * d))
@@ -155,27 +350,35 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
     DeviceInfo info;
     if ((st = b200(&dev, &info)) != GQA_OK) return st;
     if (total_q == 0) return GQA_OK;
-    gqa::AttnParams p{};
-    p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint16_t*>(k);
-    p.v = static_cast<const uint16_t*>(v);
-    p.q_stride = q_row_stride;
-    p.k_stride = k_row_stride;
-    p.v_stride = v_row_stride;
+    gqa::ServeParams p{};
+    const long long queries = ceil_div(total_q, B);
+    fill_common(&p, B, Hq, Hk, scale, queries);
     p.cu_q = cu_seqlens_q;
     p.cu_k = cu_seqlens_k;
-    p.out = out;
-    p.out_bf16 = out_dtype == GQA_OUT_BF16;
-    p.lse = lse;
-    p.B = B;
     p.total_q = total_q;
     p.total_k = total_k;
-    p.Hq = Hq;
-    p.Hk = Hk;
-    p.d = d;
-    p.scale = scale;
     p.causal = causal ? 1 : 0;
-    return launched(gqa::launch_attn_varlen(p, static_cast<cudaStream_t>(stream)));
+    p.out = out_dtype == GQA_OUT_F32 ? static_cast<float*>(out) : nullptr;
+    p.out_bf16 = out_dtype == GQA_OUT_BF16 ? static_cast<uint16_t*>(out) : nullptr;
+    p.lse = lse;
+    const int g = p.g, M = gqa::kServeBlockM;
+    const int box_h = p.pack ? g : 1, box_s = p.pos_per_tile;
+    if (!encode(&p.tm_q, q, 1, total_q, Hq, d, q_row_stride * 2, box_h, box_s) ||
+        !encode(&p.tm_o, out, 1, total_q, Hq, d, (long long)Hq * d * (p.out ? 4 : 2), box_h, box_s, p.out != nullptr))
+        return GQA_ERR_CUDA;
+    // (without keys nothing is loaded: any mapped address serves)
+    const bool keys = total_k > 0;
+    if (!encode(&p.tm_k, keys ? k : q, 1, keys ? total_k : 1, keys ? Hk : 1, d, keys ? k_row_stride * 2 : 256, 1, M) ||
+        !encode(&p.tm_v, keys ? v : q, 1, keys ? total_k : 1, keys ? Hk : 1, d, keys ? v_row_stride * 2 : 256, 1, M))
+        return GQA_ERR_CUDA;
+    // Two-tile units from a list when the average sequence fills them and there are a few per SM;
+    // else ranges over one-tile units, which also share a long key axis among CTAs.
+    const long long tiles = ceil_div(queries, p.pos_per_tile);
+    const long long units = ceil_div(total_q, 2 * p.pos_per_tile) * p.n_hg;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tiles >= 2 && units >= 3ll * info.sms) return run_list(&p, dev, info.sms, d, s);
+    p.kv_shared = (tiles > 1 || !p.pack) ? 1 : 0;
+    return run_ranges(&p, dev, info.sms, d, 1, s);
 }
 
 gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -183,9 +386,9 @@ gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_c
                              int page_size, const int* cache_seqlens, const int* tree_mask,
                              int mask_shared, const int* tree_lens, void* out, int out_dtype,
                              float* lse, int B, int T, int Sk, int Hq, int Hk, int d, float scale,
-                             int num_splits, void* stream) {
+                             void* stream) {
     if (B < 1 || T < 1) return GQA_ERR_SHAPE;
-    gqa_status st = check_heads(Hq, Hk, d, scale, out_dtype, num_splits);
+    gqa_status st = check_heads(Hq, Hk, d, scale, out_dtype);
     if (st != GQA_OK) return st;
     if (!q || !k_cache || !v_cache || !cache_seqlens || !tree_mask || !out || !lse) return GQA_ERR_NULL;
     // kernel row indices and tensor-map coordinates are 32-bit
@@ -205,30 +408,42 @@ gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_c
     int dev = 0;
     DeviceInfo info;
     if ((st = b200(&dev, &info)) != GQA_OK) return st;
-    gqa::AttnParams p{};
-    p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint16_t*>(k_cache);
-    p.v = static_cast<const uint16_t*>(v_cache);
-    p.table = block_table;
-    p.M = max_pages_per_seq;
-    p.P = num_pages;
-    p.page_shift = block_table != nullptr ? log2_of(page_size) : 0;
-    p.Sk = Sk;
+    gqa::ServeParams p{};
+    fill_common(&p, B, Hq, Hk, scale, T);
     p.seqlens = cache_seqlens;
     p.tree_lens = tree_lens;
     p.mask = tree_mask;
     p.T = T;
     p.W = (T + 31) / 32;
     p.mask_stride = mask_shared ? 0 : (long long)T * p.W;
-    p.out = out;
-    p.out_bf16 = out_dtype == GQA_OUT_BF16;
+    p.out = out_dtype == GQA_OUT_F32 ? static_cast<float*>(out) : nullptr;
+    p.out_bf16 = out_dtype == GQA_OUT_BF16 ? static_cast<uint16_t*>(out) : nullptr;
     p.lse = lse;
-    p.B = B;
-    p.Hq = Hq;
-    p.Hk = Hk;
-    p.d = d;
-    p.scale = scale;
-    return launched(gqa::launch_attn_tree(p, static_cast<cudaStream_t>(stream)));
+    const long long tiles = ceil_div(T, p.pos_per_tile);
+    const int nt = tiles >= 2 ? 2 : 1, M = gqa::kServeBlockM;
+    const int box_h = p.pack ? p.g : 1, box_s = p.pos_per_tile;
+    if (!encode(&p.tm_q, q, B, T, Hq, d, 2ll * Hq * d, box_h, box_s) ||
+        !encode(&p.tm_o, out, B, T, Hq, d, (long long)Hq * d * (p.out ? 4 : 2), box_h, box_s, p.out != nullptr))
+        return GQA_ERR_CUDA;
+    const long long kv_row = 2ll * Hk * d;
+    if (block_table == nullptr) {
+        p.cap = Sk;
+        if (!encode(&p.tm_k, k_cache, B, Sk, Hk, d, kv_row, 1, M) || !encode(&p.tm_v, v_cache, B, Sk, Hk, d, kv_row, 1, M))
+            return GQA_ERR_CUDA;
+    } else {
+        // the page pools as (d, Hk, page_size, num_pages), boxes of up to 128 rows
+        p.cap = max_pages_per_seq * page_size;
+        p.block_table = block_table;
+        p.table_stride = max_pages_per_seq;
+        p.page_shift = log2_of(page_size);
+        p.page_rows = page_size < M ? page_size : M;
+        p.num_pages = num_pages;
+        if (!encode(&p.tm_k, k_cache, num_pages, page_size, Hk, d, kv_row, 1, p.page_rows) ||
+            !encode(&p.tm_v, v_cache, num_pages, page_size, Hk, d, kv_row, 1, p.page_rows))
+            return GQA_ERR_CUDA;
+    }
+    p.kv_shared = (tiles > nt || !p.pack) ? 1 : 0;
+    return run_ranges(&p, dev, info.sms, d, nt, static_cast<cudaStream_t>(stream));
 }
 
 gqa_status gqa_cache_resize(int* block_table, int* cache_seqlens, int* page_refs, int S,
@@ -297,8 +512,15 @@ gqa_status gqa_cache_compact(void* k_pages, void* v_pages, int layers, long long
 }
 
 gqa_status gqa_serve_device_status(int reset) {
-    (void)reset;
-    return GQA_OK;
+    unsigned int* ptr = gqa::serve_status_symbol();
+    if (!ptr) return GQA_ERR_CUDA;
+    unsigned int h = 0;
+    if (cudaMemcpy(&h, ptr, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return GQA_ERR_CUDA;
+    if (reset) {
+        const unsigned int z = 0;
+        if (cudaMemcpy(ptr, &z, sizeof(z), cudaMemcpyHostToDevice) != cudaSuccess) return GQA_ERR_CUDA;
+    }
+    return h ? GQA_ERR_TIMEOUT : GQA_OK;
 }
 
 }  // extern "C"

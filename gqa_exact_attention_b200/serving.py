@@ -49,8 +49,8 @@ def load_serve():
         raise RuntimeError(f"libgqa_serve.so not found at {serve_lib_path}; run the package build")
     L = ctypes.CDLL(serve_lib_path)
     i, f, p, ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
-    L.gqa_attn_fwd_varlen.argtypes = [p, ll, p, ll, p, ll, p, p, p, i, p, i, i, i, i, i, i, f, i, i, p]
-    L.gqa_attn_fwd_tree.argtypes = [p, p, p, p, i, i, i, p, p, i, p, p, i, p, i, i, i, i, i, i, f, i, p]
+    L.gqa_attn_fwd_varlen.argtypes = [p, ll, p, ll, p, ll, p, p, p, i, p, i, i, i, i, i, i, f, i, p]
+    L.gqa_attn_fwd_tree.argtypes = [p, p, p, p, i, i, i, p, p, i, p, p, i, p, i, i, i, i, i, i, f, p]
     L.gqa_cache_resize.argtypes = [p, p, p, i, i, i, i, p, p, i, p, p]
     L.gqa_cache_fork.argtypes = [p, p, i, ll, p, p, p, i, i, i, i, p, p, i, p, p]
     L.gqa_cache_compact.argtypes = [p, p, i, ll, p, p, p, i, i, i, i, p, p, p, i, p, p]
@@ -110,7 +110,7 @@ def _stream(stream, device):
 
 
 def gqa_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=None,
-                        out_dtype=None, scale=None, causal=False, num_splits=0, stream=None):
+                        out_dtype=None, scale=None, causal=False, stream=None):
     """out, lse = gqa_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, ...).
 
     q: bf16 [total_q, Hq, d]; k, v: bf16 [total_k, Hk, d]: sequences one behind the other, rows
@@ -146,13 +146,12 @@ def gqa_attn_fwd_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, out=None, lse=
         _check(load_serve().gqa_attn_fwd_varlen(
             q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cq, ck, out.data_ptr(), code,
             lse.data_ptr(), B, total_q, total_k, Hq, Hk, d, float(scale), int(bool(causal)),
-            int(num_splits), _stream(stream, q.device)))
+            _stream(stream, q.device)))
     return out, lse
 
 
 def gqa_attn_fwd_tree(q, k_cache, v_cache, tree_mask, cache_seqlens, block_table=None,
-                      tree_lens=None, out=None, lse=None, out_dtype=None, scale=None,
-                      num_splits=0, stream=None):
+                      tree_lens=None, out=None, lse=None, out_dtype=None, scale=None, stream=None):
     """out, lse = gqa_attn_fwd_tree(q, k_cache, v_cache, tree_mask, cache_seqlens, ...).
 
     q: bf16 [B, T, Hq, d], the drafted nodes' queries; their keys are the last of each
@@ -195,7 +194,7 @@ def gqa_attn_fwd_tree(q, k_cache, v_cache, tree_mask, cache_seqlens, block_table
         _check(load_serve().gqa_attn_fwd_tree(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), tb, M, P, page, ls, mk,
             int(shared), tl, out.data_ptr(), code, lse.data_ptr(), B, T, Sk, Hq, Hk, d,
-            float(scale), int(num_splits), _stream(stream, q.device)))
+            float(scale), _stream(stream, q.device)))
     return out, lse
 
 

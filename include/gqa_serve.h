@@ -38,8 +38,6 @@ extern "C" {
  *        sees key j iff j <= i + Lk - Lq.  A row that sees no key gets out = 0, lse = -inf.
  *   out  fp32 or bf16 [total_q, Hq, d] (out_dtype as in gqa_attn_fwd_kvcache).
  *   lse  fp32 [Hq, total_q].  Rows that belong to no sequence are left as they were, in both.
- *   num_splits   0 = chosen from B, total_q and total_k; >= 1 = that many key ranges per
- *        sequence (clamped to 16), joined in a second pass.
  *
  * What other sequences hold does not reach a sequence's result, not even infinities or NaN.
  * Within a sequence a value of V that is not finite reaches every row of its 128-key block,
@@ -54,8 +52,7 @@ GQA_API gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, co
                                        long long v_row_stride, const int* cu_seqlens_q,
                                        const int* cu_seqlens_k, void* out, int out_dtype,
                                        float* lse, int B, int total_q, int total_k, int Hq,
-                                       int Hk, int d, float scale, int causal, int num_splits,
-                                       void* stream);
+                                       int Hk, int d, float scale, int causal, void* stream);
 
 /*
  * gqa_attn_fwd_tree — attention of T drafted tokens per sequence, arranged as a tree, over a
@@ -77,7 +74,6 @@ GQA_API gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, co
  *                   nodes >= n_b are ignored.
  *   out, lse        [B, T, Hq, d] and [B, Hq, T].  A row that sees no key, and rows i >= n_b,
  *                   get out = 0 and lse = -inf.
- *   num_splits      as gqa_attn_fwd_kvcache.
  *
  * Keys at or past L_b do not reach the result, whatever they hold.  A table entry outside
  * [0, num_pages) reads as a page of zeros.  Errors as gqa_attn_fwd_paged; GQA_ERR_NULL for a
@@ -89,7 +85,7 @@ GQA_API gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const v
                                      int page_size, const int* cache_seqlens, const int* tree_mask,
                                      int mask_shared, const int* tree_lens, void* out,
                                      int out_dtype, float* lse, int B, int T, int Sk, int Hq,
-                                     int Hk, int d, float scale, int num_splits, void* stream);
+                                     int Hk, int d, float scale, void* stream);
 
 /*
  * The pages of a cache.  Their state is three device int32 arrays of the caller's:

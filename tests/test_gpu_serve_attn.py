@@ -48,15 +48,14 @@ def varlen_ref(q, k, v, cq, ck, causal, scale):
     return out, lse, tol, ltol, inside
 
 
-def run_varlen(rng, lq, lk, Hq, Hk, d, causal, splits=0, bf16=False, start=0, after=0, scale=None):
+def run_varlen(rng, lq, lk, Hq, Hk, d, causal, bf16=False, start=0, after=0, scale=None):
     tq, tk = start + sum(lq) + after, start + sum(lk) + after
     q, k, v = randn(rng, tq, Hq, d), randn(rng, tk, Hk, d), randn(rng, tk, Hk, d)
     cq, ck = cu(lq, start), cu(lk, start)
     dt = torch.bfloat16 if bf16 else torch.float32
     out = torch.full((tq, Hq, d), 7.0, dtype=dt, device="cuda")
     lse = torch.full((Hq, tq), 7.0, device="cuda")
-    G.gqa_attn_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), cq, ck, out=out, lse=lse, causal=causal,
-                          num_splits=splits, scale=scale)
+    G.gqa_attn_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), cq, ck, out=out, lse=lse, causal=causal, scale=scale)
     torch.cuda.synchronize()
     s = d ** -0.5 if scale is None else scale
     o, l, tol, ltol, inside = varlen_ref(f64(q), f64(k), f64(v), cq.cpu().numpy(), ck.cpu().numpy(), causal, s)
@@ -85,17 +84,17 @@ VARLEN = [
 
 @pytest.mark.parametrize("case", range(len(VARLEN)))
 @pytest.mark.parametrize("causal", [False, True])
-@pytest.mark.parametrize("splits", [0, 1, 3])
-def test_varlen(case, causal, splits):
+@pytest.mark.parametrize("bf16", [False, True])
+def test_varlen(case, causal, bf16):
     lq, lk, Hq, Hk, d = VARLEN[case]
     rng = np.random.default_rng(100 + case)
-    run_varlen(rng, lq, lk or lq, Hq, Hk, d, causal, splits, bf16=bool((case + splits) & 1))
+    run_varlen(rng, lq, lk or lq, Hq, Hk, d, causal, bf16)
 
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_varlen_rows_outside_the_sequences_stay(d, bf16):
-    run_varlen(np.random.default_rng(7), [70, 0, 200, 3], [70, 5, 210, 3], 8, 2, d, True, 0, bf16, start=5, after=150)
+    run_varlen(np.random.default_rng(7), [70, 0, 200, 3], [70, 5, 210, 3], 8, 2, d, True, bf16, start=5, after=150)
 
 
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 2.5])
@@ -103,11 +102,21 @@ def test_varlen_scales(scale):
     run_varlen(np.random.default_rng(8), [150, 40], [150, 300], 4, 2, 64, True, scale=scale)
 
 
-@pytest.mark.parametrize("splits", [0, 2])
-def test_varlen_many_sequences(splits):
+@pytest.mark.parametrize("B", [700, 1500])
+def test_varlen_many_sequences(B):
     rng = np.random.default_rng(9)
-    lens = [int(x) for x in rng.integers(0, 40, 700)]
-    run_varlen(rng, lens, lens, 4, 2, 64, True, splits)
+    lens = [int(x) for x in rng.integers(0, 40, B)]
+    run_varlen(rng, lens, lens, 4, 2, 64, True)
+
+
+@pytest.mark.parametrize("Hq,Hk,d", [(32, 32, 128), (64, 8, 64), (24, 8, 128), (32, 8, 64)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_varlen_many_tiles(Hq, Hk, d, causal):
+    """Enough tiles for several rounds of two-tile units on every SM, of ragged sequences."""
+    rng = np.random.default_rng(15)
+    lens = [800, 0, 1100, 5, 700, 257, 512, 1, 640, 900]
+    run_varlen(rng, lens, lens, Hq, Hk, d, causal, bf16=True, start=3, after=70)
+    run_varlen(rng, lens, [x + 100 * (i % 3) for i, x in enumerate(lens)], Hq, Hk, d, causal)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -196,7 +205,7 @@ def tree(rng, T):
     return see
 
 
-def run_tree(rng, lens, T, Hq, Hk, d, page, n=None, see=None, shared=False, splits=0, bf16=False, cap=None,
+def run_tree(rng, lens, T, Hq, Hk, d, page, n=None, see=None, shared=False, bf16=False, cap=None,
              poison=True):
     B = len(lens)
     cap = cap or max(max(lens), 1) + 5
@@ -211,7 +220,7 @@ def run_tree(rng, lens, T, Hq, Hk, d, page, n=None, see=None, shared=False, spli
             for b, L in enumerate(lens):
                 x[b, L:] = bad
     args = dict(tree_lens=None if n is None else torch.tensor(n, dtype=torch.int32, device="cuda"),
-                out_dtype=torch.bfloat16 if bf16 else torch.float32, num_splits=splits)
+                out_dtype=torch.bfloat16 if bf16 else torch.float32)
     if page:
         M = -(-cap // page)
         perm = rng.permutation(B * M + 3)
@@ -258,11 +267,10 @@ TREE = [
 
 @pytest.mark.parametrize("case", range(len(TREE)))
 @pytest.mark.parametrize("page", [0, 16, 64, 256])
-@pytest.mark.parametrize("splits", [0, 3])
-def test_tree(case, page, splits):
+@pytest.mark.parametrize("bf16", [False, True])
+def test_tree(case, page, bf16):
     lens, T, Hq, Hk, d = TREE[case]
-    run_tree(np.random.default_rng(200 + case), lens, T, Hq, Hk, d, page, splits=splits,
-             bf16=bool((case + splits) & 1))
+    run_tree(np.random.default_rng(200 + case), lens, T, Hq, Hk, d, page, bf16=bf16)
 
 
 @pytest.mark.parametrize("page", [0, 32])
@@ -326,46 +334,45 @@ def test_tree_entry_outside_the_pool_reads_zeros():
 
 # ---------------------------------------------------------------- streams, graphs, repeats
 
-def _both(rng):
-    lens = [300, 17, 128, 999]
-    q, k, v = (randn(rng, sum(lens), H, 128).cuda() for H in (8, 2, 2))
+def _both(rng, scale=1):
+    lens = [scale * x for x in (300, 17, 128, 999)]
+    q, k, v = (randn(rng, sum(lens), H, 128).cuda() for H in (32, 8, 8))
     c = cu(lens)
     tq = randn(rng, 3, 10, 8, 128).cuda()
     kc, vc = randn(rng, 3, 700, 2, 128).cuda(), randn(rng, 3, 700, 2, 128).cuda()
     mask = bits(np.stack([tree(rng, 10) for _ in range(3)]))
     sl = torch.tensor([700, 10, 400], dtype=torch.int32, device="cuda")
 
-    def call(splits=0):
-        return (*G.gqa_attn_fwd_varlen(q, k, v, c, causal=True, num_splits=splits),
-                *G.gqa_attn_fwd_tree(tq, kc, vc, mask, sl, num_splits=splits))
+    def call():
+        return (*G.gqa_attn_fwd_varlen(q, k, v, c, causal=True), *G.gqa_attn_fwd_tree(tq, kc, vc, mask, sl))
     return call, (q, tq)
 
 
-@pytest.mark.parametrize("splits", [0, 1, 2])
-def test_repeats_and_other_streams_give_the_same_bits(splits):
-    call, _ = _both(np.random.default_rng(40))
-    want = call(splits)
+@pytest.mark.parametrize("scale", [1, 4])
+def test_repeats_and_other_streams_give_the_same_bits(scale):
+    call, _ = _both(np.random.default_rng(40), scale)
+    want = call()
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
-        got = call(splits)
-    again = call(splits)  # at the same time as the other stream's
+        got = call()
+    again = call()  # at the same time as the other stream's
     torch.cuda.synchronize()
     for a, b, c in zip(want, got, again):
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
-@pytest.mark.parametrize("splits", [0, 2])
-def test_captured_graphs(splits):
+@pytest.mark.parametrize("scale", [1, 4])
+def test_captured_graphs(scale):
     """Two graphs, replayed in turn and at once with new inputs, give what the calls give."""
     pairs = []
     for seed in (41, 42):
-        call, inputs = _both(np.random.default_rng(seed))
-        call(splits)
+        call, inputs = _both(np.random.default_rng(seed), scale)
+        call()
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            got = call(splits)
+            got = call()
         pairs.append((call, inputs, graph, got))
     for _, inputs, _, _ in pairs:
         for x in inputs:
@@ -378,5 +385,5 @@ def test_captured_graphs(splits):
                 graph.replay()
     torch.cuda.synchronize()
     for call, _, _, got in pairs:
-        for a, b in zip(got, call(splits)):
+        for a, b in zip(got, call()):
             assert torch.equal(a, b)

@@ -41,16 +41,16 @@ NO_GPU = (6, 8)
 
 
 def varlen(q=16, qs=0, k=16, ks=0, v=16, vs=0, cq=16, ck=16, out=16, dt=0, lse=16, B=2, tq=8, tk=8, Hq=4, Hk=2,
-           d=64, scale=0.125, causal=1, splits=0):
+           d=64, scale=0.125, causal=1):
     return G.load_serve().gqa_attn_fwd_varlen(q, qs, k, ks, v, vs, cq, ck, out, dt, lse, B, tq, tk, Hq, Hk, d,
-                                              scale, causal, splits, None)
+                                              scale, causal, None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(q=NULL), 1), (dict(k=NULL), 1), (dict(v=NULL), 1), (dict(cq=NULL), 1), (dict(ck=NULL), 1),
     (dict(out=NULL), 1), (dict(lse=NULL), 1),
     (dict(B=0), 2), (dict(tq=-1), 2), (dict(tk=-1), 2), (dict(Hq=0), 2), (dict(Hk=0), 2), (dict(dt=2), 2),
-    (dict(splits=-1), 2), (dict(scale=float("nan")), 2),
+    (dict(scale=float("nan")), 2),
     (dict(qs=255), 2), (dict(qs=260), 2), (dict(ks=120), 2), (dict(vs=64), 2), (dict(qs=-256), 2), (dict(ks=1 << 40), 2),
     (dict(tq=1 << 30), 2), (dict(tk=1 << 30), 2),
     (dict(Hq=6, Hk=4), 3), (dict(d=96), 4), (dict(q=24), 5), (dict(out=8), 5), (dict(cq=18), 5), (dict(ck=17), 5),
@@ -60,16 +60,16 @@ def test_varlen_refusals(kw, code):
 
 
 def tree(q=16, k=16, v=16, table=16, M=4, P=8, page=16, lens=16, mask=16, shared=0, tl=NULL, out=16, dt=0, lse=16,
-         B=2, T=4, Sk=0, Hq=4, Hk=2, d=64, scale=0.125, splits=0):
+         B=2, T=4, Sk=0, Hq=4, Hk=2, d=64, scale=0.125):
     return G.load_serve().gqa_attn_fwd_tree(q, k, v, table, M, P, page, lens, mask, shared, tl, out, dt, lse, B, T,
-                                            Sk, Hq, Hk, d, scale, splits, None)
+                                            Sk, Hq, Hk, d, scale, None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(q=NULL), 1), (dict(k=NULL), 1), (dict(v=NULL), 1), (dict(lens=NULL), 1), (dict(mask=NULL), 1),
     (dict(out=NULL), 1), (dict(lse=NULL), 1),
     (dict(B=0), 2), (dict(T=0), 2), (dict(M=0), 2), (dict(P=0), 2), (dict(page=8), 2), (dict(page=48), 2),
-    (dict(dt=-1), 2), (dict(splits=-2), 2), (dict(scale=float("inf")), 2), (dict(table=NULL, Sk=0), 2),
+    (dict(dt=-1), 2), (dict(scale=float("inf")), 2), (dict(table=NULL, Sk=0), 2),
     (dict(M=1 << 27), 2), (dict(P=1 << 27), 2), (dict(B=1 << 20, T=1 << 10), 2), (dict(table=NULL, Sk=1 << 30), 2),
     (dict(Hq=5), 3), (dict(d=80), 4),
     (dict(q=8), 5), (dict(table=18), 5), (dict(lens=17), 5), (dict(mask=18), 5), (dict(tl=18), 5),
