@@ -98,9 +98,12 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
     const int rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheState& c = p.c;
+    if constexpr (FORK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int n = p.n;
     const int size = set_size(n);
-    int* upto = smem;       // [n] pages needed by requests 0..i
+    int* key_ = smem;       // [n] the requests
+    int* arg_ = key_ + n;
+    int* upto = arg_ + n;   // [n] pages needed by requests 0..i
     int* first = upto + n;  // [n] the first new entry of request i's row
     int* old = first + n;   // [n] entries that request i gives up end here
     int* state = old + n;   // [n] GQA_CACHE_DONE, _INVALID, _SHARED, or one of
@@ -110,7 +113,6 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
     const SlotSet keys{state + n, state + n + size, size - 1};
     const SlotSet parents{state + n + 2 * size, state + n + 3 * size, size - 1};  // fork only
 
-    auto key_of = [&](int i) { return p.key != nullptr ? p.key[i] : i; };
 
     // ---- 1. the requests, by every block alike (nothing of the state changes yet)
     for (int i = tid; i < size; i += kThreads) {
@@ -121,12 +123,16 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
             parents.first[i] = 0x7fffffff;
         }
     }
+    for (int i = tid; i < n; i += kThreads) {
+        key_[i] = p.key != nullptr ? p.key[i] : i;
+        arg_[i] = p.arg[i];
+    }
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
-        const int key = key_of(i);
+        const int key = key_[i], arg = arg_[i];
         if (key >= 0 && key < c.S) keys.insert(key, i);
         if constexpr (FORK) {
-            if (p.arg[i] >= 0 && p.arg[i] < c.S) parents.insert(p.arg[i], i);
+            if (arg >= 0 && arg < c.S) parents.insert(arg, i);
         }
     }
     __syncthreads();
@@ -136,7 +142,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         const int i = r * kThreads + tid;
         int need = 0;
         if (i < n) {
-            const int key = key_of(i), arg = p.arg[i];
+            const int key = key_[i], arg = arg_[i];
             int st = GQA_CACHE_INVALID, at = 0, end = 0;
             if (key >= 0 && key < c.S && keys.find(key) == i) {
                 const int mine = clamp_len(c.lens[key], c);
@@ -187,8 +193,8 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         const int lo = FORK ? 0 : first[i];
         const int hi = FORK ? max(first[i], old[i]) : old[i];
         if (j0 >= hi || j0 + kChunk <= lo) continue;
-        int* row = row_of(c, key_of(i));
-        const int* from = FORK ? row_of(c, p.arg[i]) : nullptr;
+        int* row = row_of(c, key_[i]);
+        const int* from = FORK ? row_of(c, arg_[i]) : nullptr;
         int was[kChunk / 32], now[kChunk / 32];
 #pragma unroll
         for (int e = 0; e < kChunk / 32; ++e) {
@@ -205,19 +211,36 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         }
     }
 
-    // ---- 3. the free pages, counted per warp over its own range of page numbers
+    // ---- 3. the free pages, counted per warp over its own range of page numbers, kFew * 32 at a
+    // time so that the loads overlap; bit e of a lane's mask is page 32 e + lane
+    constexpr int kFew = 32;
     int free_before = 0, free_all = 0;
     const int per_warp = ((c.P + kClusterCtas * kWarps - 1) / (kClusterCtas * kWarps) + 31) / 32 * 32;
     const long long p0 = (long long)(rank * kWarps + warp) * per_warp;
     const int p_lo = p0 < c.P ? (int)p0 : c.P;
     const int p_hi = p0 + per_warp < c.P ? (int)(p0 + per_warp) : c.P;
+    auto free_mask = [&](int at) {
+        int x[kFew];
+        unsigned m = 0;
+#pragma unroll
+        for (int e = 0; e < kFew; ++e) {
+            const int page = at + e * 32 + lane;
+            x[e] = page < p_hi ? __ldcg(c.refs + page) : 1;
+        }
+#pragma unroll
+        for (int e = 0; e < kFew; ++e) m |= x[e] == 0 ? 1u << e : 0u;
+        return m;
+    };
     if (needed > 0) {
         cluster.sync();  // the counts are final
         int mine = 0;
-        for (int at = p_lo; at < p_hi; at += 32) {
-            const int page = at + lane;
-            mine += __popc(__ballot_sync(0xffffffffu, page < p_hi && __ldcg(c.refs + page) == 0));
+        unsigned first_mask = 0;  // of the warp's first pages: most pools have no more
+        for (int at = p_lo; at < p_hi; at += kFew * 32) {
+            const unsigned m = free_mask(at);
+            if (at == p_lo) first_mask = m;
+            mine += __popc(m);
         }
+        mine = __reduce_add_sync(0xffffffffu, mine);
         long long total;
         const int incl = (int)block_scan(lane == 31 ? mine : 0, warp_sums, &total);
         // (lane 31 of each warp holds the sum up to and with its warp)
@@ -231,23 +254,27 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         }
 
         // ---- 4. each warp hands out its own free pages
-        for (int at = p_lo; at < p_hi && free_before < needed; at += 32) {
-            const int page = at + lane;
-            const bool is_free = page < p_hi && __ldcg(c.refs + page) == 0;
-            const unsigned ball = __ballot_sync(0xffffffffu, is_free);
-            const int r = free_before + __popc(ball & ((1u << lane) - 1u));
-            free_before += __popc(ball);
-            if (is_free && r < needed) {
-                int lo = 0, hi = n - 1;  // the first request with upto > r
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (upto[mid] > r) hi = mid;
-                    else lo = mid + 1;
-                }
-                if (upto[lo] <= free_all) {
-                    const int before = lo > 0 ? upto[lo - 1] : 0;
-                    row_of(c, key_of(lo))[first[lo] + (r - before)] = page;
-                    c.refs[page] = 1;
+        for (int at = p_lo; at < p_hi && free_before < needed; at += kFew * 32) {
+            const unsigned m = at == p_lo ? first_mask : free_mask(at);
+#pragma unroll 1
+            for (int e = 0; e < kFew && free_before < needed; ++e) {
+                const bool is_free = (m >> e) & 1u;
+                const unsigned ball = __ballot_sync(0xffffffffu, is_free);
+                const int r = free_before + __popc(ball & ((1u << lane) - 1u));
+                free_before += __popc(ball);
+                if (is_free && r < needed) {
+                    int lo = 0, hi = n - 1;  // the first request with upto > r
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        if (upto[mid] > r) hi = mid;
+                        else lo = mid + 1;
+                    }
+                    if (upto[lo] <= free_all) {
+                        const int before = lo > 0 ? upto[lo - 1] : 0;
+                        const int page = at + e * 32 + lane;
+                        row_of(c, key_[lo])[first[lo] + (r - before)] = page;
+                        c.refs[page] = 1;
+                    }
                 }
             }
         }
@@ -259,9 +286,9 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         if (st == kTake) st = upto[i] <= free_all ? GQA_CACHE_DONE : GQA_CACHE_NO_PAGES;
         if constexpr (FORK) {
             if (acts(i))
-                c.lens[p.key[i]] = st == GQA_CACHE_DONE ? clamp_len(c.lens[p.arg[i]], c) : 0;
+                c.lens[key_[i]] = st == GQA_CACHE_DONE ? clamp_len(c.lens[arg_[i]], c) : 0;
         } else {
-            if (st == GQA_CACHE_DONE) c.lens[key_of(i)] = p.arg[i];
+            if (st == GQA_CACHE_DONE) c.lens[key_[i]] = arg_[i];
         }
         p.status[i] = st == kSkip ? (int)GQA_CACHE_DONE : st;
     }
@@ -271,7 +298,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
             cluster.sync();  // no warp looks for free pages any more
             for (int i = rank * kWarps + warp; i < n; i += kClusterCtas * kWarps) {
                 if (state[i] != kTake || upto[i] <= free_all) continue;
-                int* row = row_of(c, p.key[i]);
+                int* row = row_of(c, key_[i]);
                 for (int j = lane; j < first[i]; j += 32) {
                     if (known(row[j], c)) atomicSub(c.refs + row[j], 1);
                     row[j] = -1;
@@ -282,38 +309,46 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
     if (needed > 0) cluster.sync();  // a block's count is read by the others until here
 }
 
-// The last rows of each fork: [0, len % page) of the parent's last page to the child's, in
-// every layer's K and V.  A unit is 16 KB of one page; units past a fork's rows end at once.
+// The last rows of each fork: [0, len % page) of the parent's last page to the child's, in every
+// layer's K and V.  A block belongs to one fork (blockIdx.x) and takes every gridDim.y-th of its
+// pieces, 16 KB of one page in one layer; what it has to look up, it looks up once.  Bound by the
+// bytes: a parent's rows are read from DRAM once and by its other children from L2.
 constexpr int kCopyBytes = 16384;
 constexpr int kCopyThreads = 256;
 
 __global__ void __launch_bounds__(kCopyThreads) cache_tail_copy_kernel(const __grid_constant__ PlanParams p,
-                                                                       const __grid_constant__ Pools pools,
-                                                                       int parts) {
+                                                                       const __grid_constant__ Pools pools) {
     const CacheState& c = p.c;
-    const long long units = (long long)p.n * pools.layers * 2 * parts;
+    const int i = blockIdx.x;
+    const int child = p.key[i], parent = p.arg[i];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is done
+    if (p.status[i] != GQA_CACHE_DONE || parent == child) return;
+    const int len = clamp_len(__ldcg(c.lens + child), c);
+    const int tail = len & ((1 << c.page_shift) - 1);
+    if (tail == 0) return;
+    const int entry = len >> c.page_shift;
+    const int src = __ldcg(row_of(c, parent) + entry), dst = __ldcg(row_of(c, child) + entry);
+    if (!known(src, c) || !known(dst, c)) return;
     const long long page_bytes = pools.row_bytes << c.page_shift;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const int part = (int)(u % parts);
-        const int kv = (int)(u / parts % 2);
-        const int layer = (int)(u / (2ll * parts) % pools.layers);
-        const int i = (int)(u / (2ll * parts * pools.layers));
-        if (p.status[i] != GQA_CACHE_DONE || p.arg[i] == p.key[i]) continue;
-        const int len = clamp_len(c.lens[p.key[i]], c);
-        const int tail = len & ((1 << c.page_shift) - 1);
-        const long long bytes = tail * pools.row_bytes;
-        if ((long long)part * kCopyBytes >= bytes) continue;
-        const int entry = len >> c.page_shift;
-        const int src = row_of(c, p.arg[i])[entry], dst = row_of(c, p.key[i])[entry];
-        if (!known(src, c) || !known(dst, c)) continue;
+    const long long bytes = tail * pools.row_bytes;
+    const int parts = (int)((bytes + kCopyBytes - 1) / kCopyBytes);
+    const int pieces = pools.layers * 2 * parts;
+    for (int x = blockIdx.y; x < pieces; x += gridDim.y) {
+        const int part = x % parts, kv = x / parts & 1, layer = x / parts / 2;
         uint8_t* pool = pools.kv[kv] + (size_t)layer * c.P * page_bytes;
         const uint8_t* from = pool + (size_t)src * page_bytes;
         uint8_t* to = pool + (size_t)dst * page_bytes;
+        constexpr int kEach = kCopyBytes / (16 * kCopyThreads);
+        uint4 v[kEach];
 #pragma unroll
-        for (int e = 0; e < kCopyBytes / (16 * kCopyThreads); ++e) {
+        for (int e = 0; e < kEach; ++e) {
             const long long at = (long long)part * kCopyBytes + (e * kCopyThreads + threadIdx.x) * 16;
-            if (at < bytes)
-                *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+            if (at < bytes) v[e] = *reinterpret_cast<const uint4*>(from + at);
+        }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const long long at = (long long)part * kCopyBytes + (e * kCopyThreads + threadIdx.x) * 16;
+            if (at < bytes) *reinterpret_cast<uint4*>(to + at) = v[e];
         }
     }
 }
@@ -354,48 +389,56 @@ __device__ CompactSlot compact_slot(const CompactParams& p, int s) {
 
 // Moves the accepted rows.  A thread owns one 16-byte column of one layer's K or V and walks
 // the accepted nodes in order: node keep[j] >= j goes to place j, so a row is overwritten only
-// after it was read, and eight rows may be read before their eight writes.
+// after it was read, and eight rows may be read before their eight writes.  The rows' places are
+// looked up by the block together, kMoveRows at a time.
 constexpr int kMoveThreads = 128;
 constexpr int kMoveBatch = 8;
+constexpr int kMoveRows = 128;
 __global__ void __launch_bounds__(kMoveThreads) cache_compact_rows_kernel(const __grid_constant__ CompactParams p) {
+    __shared__ int from_[kMoveRows], to_[kMoveRows];  // rows of a layer's pool; -1: not moved
     const CacheState& c = p.c;
     const int s = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const CompactSlot r = compact_slot(p, s);
     if (blockIdx.y == 0 && threadIdx.x == 0) p.status[s] = r.status;
     if (r.status != GQA_CACHE_DONE) return;
     const int cols = (int)(p.pools.row_bytes / 16);
-    const long long item = (long long)blockIdx.y * kMoveThreads + threadIdx.x;
-    if (item >= 2ll * p.pools.layers * cols) return;
-    const int col = (int)(item % cols);
-    const int kv = (int)(item / cols % 2), layer = (int)(item / cols / 2);
-    uint8_t* pool = p.pools.kv[kv] + ((size_t)layer * c.P << c.page_shift) * p.pools.row_bytes + (size_t)col * 16;
+    const int items = 2 * p.pools.layers * cols;
     const int* row = row_of(c, s);
     const int* keep = p.keep + (size_t)s * p.T;
     const int in_page = (1 << c.page_shift) - 1;
-    auto at = [&](int pos) -> uint8_t* {
+    auto at = [&](int pos) {
         const int page = row[pos >> c.page_shift];
-        if (!known(page, c)) return nullptr;
-        return pool + (((size_t)page << c.page_shift) + (pos & in_page)) * p.pools.row_bytes;
+        return known(page, c) ? (page << c.page_shift) + (pos & in_page) : -1;
     };
     const int m = r.end - r.base;
-    for (int j0 = 0; j0 < m; j0 += kMoveBatch) {
-        uint4 x[kMoveBatch];
-        uint8_t* to[kMoveBatch];
+    for (int j0 = 0; j0 < m; j0 += kMoveRows) {
+        const int n = min(kMoveRows, m - j0);
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += kMoveThreads) {
+            const int node = keep[j0 + j];
+            const int to = node > j0 + j ? at(r.base + j0 + j) : -1;
+            const int from = to >= 0 ? at(r.base + node) : -1;
+            from_[j] = from;
+            to_[j] = from >= 0 ? to : -1;
+        }
+        __syncthreads();
+        // (a row that the next kMoveRows read is never written by these: it lies further on)
+        for (int item = blockIdx.y * kMoveThreads + threadIdx.x; item < items; item += gridDim.y * kMoveThreads) {
+            const int col = item % cols, kv = item / cols & 1, layer = item / cols / 2;
+            uint8_t* pool = p.pools.kv[kv] + ((size_t)layer * c.P << c.page_shift) * p.pools.row_bytes + (size_t)col * 16;
+            for (int j = 0; j < n; j += kMoveBatch) {
+                uint4 x[kMoveBatch];
 #pragma unroll
-        for (int e = 0; e < kMoveBatch; ++e) {
-            to[e] = nullptr;
-            const int j = j0 + e;
-            if (j < m && keep[j] > j) {
-                const uint8_t* from = at(r.base + keep[j]);
-                if (from != nullptr) {
-                    to[e] = at(r.base + j);
-                    x[e] = *reinterpret_cast<const uint4*>(from);
-                }
+                for (int e = 0; e < kMoveBatch; ++e)
+                    if (j + e < n && from_[j + e] >= 0)
+                        x[e] = *reinterpret_cast<const uint4*>(pool + (size_t)from_[j + e] * p.pools.row_bytes);
+#pragma unroll
+                for (int e = 0; e < kMoveBatch; ++e)
+                    if (j + e < n && to_[j + e] >= 0)
+                        *reinterpret_cast<uint4*>(pool + (size_t)to_[j + e] * p.pools.row_bytes) = x[e];
             }
         }
-#pragma unroll
-        for (int e = 0; e < kMoveBatch; ++e)
-            if (to[e] != nullptr) *reinterpret_cast<uint4*>(to[e]) = x[e];
     }
 }
 
@@ -403,6 +446,7 @@ __global__ void __launch_bounds__(kMoveThreads) cache_compact_rows_kernel(const 
 __global__ void __launch_bounds__(128) cache_compact_pages_kernel(const __grid_constant__ CompactParams p) {
     const CacheState& c = p.c;
     const int s = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows have moved
     if (s >= c.S || p.status[s] != GQA_CACHE_DONE) return;
     const int len = clamp_len(c.lens[s], c);
     const int nodes = min(max(p.tree_lens != nullptr ? p.tree_lens[s] : p.T, 0), min(p.T, len));
@@ -418,7 +462,7 @@ __global__ void __launch_bounds__(128) cache_compact_pages_kernel(const __grid_c
 
 template <bool FORK>
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
-    const size_t bytes = sizeof(int) * (4 * (size_t)p.n + (FORK ? 4 : 2) * (size_t)set_size(p.n));
+    const size_t bytes = sizeof(int) * (6 * (size_t)p.n + (FORK ? 4 : 2) * (size_t)set_size(p.n));
     if (bytes > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)bytes);
@@ -432,25 +476,43 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
 
 cudaError_t launch_resize(const PlanParams& p, cudaStream_t stream) { return launch_plan<false>(p, stream); }
 
+// A kernel that may be brought in while the one before it still runs, and waits for it itself.
+template <class... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream, const A&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_fork(const PlanParams& p, const Pools& pools, int sms, cudaStream_t stream) {
     cudaError_t e = launch_plan<true>(p, stream);
     if (e != cudaSuccess) return e;
+    // about 16 blocks per SM in all, but none without a piece of a whole page
     const long long page_bytes = pools.row_bytes << p.c.page_shift;
-    const int parts = (int)((page_bytes + kCopyBytes - 1) / kCopyBytes);
-    const long long units = (long long)p.n * pools.layers * 2 * parts;
-    const long long most = (long long)sms * 8;
-    cache_tail_copy_kernel<<<(unsigned)(units < most ? units : most), kCopyThreads, 0, stream>>>(p, pools, parts);
-    return cudaGetLastError();
+    const long long pieces = (page_bytes + kCopyBytes - 1) / kCopyBytes * pools.layers * 2;
+    long long each = ((long long)sms * 16 + p.n - 1) / p.n;
+    if (each > pieces) each = pieces;
+    if (each > 65535) each = 65535;
+    return launch_after(cache_tail_copy_kernel, dim3((unsigned)p.n, (unsigned)each), kCopyThreads, stream, p, pools);
 }
 
-cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t stream) {
     const long long items = 2ll * p.pools.layers * (p.pools.row_bytes / 16);
-    const dim3 grid((unsigned)p.c.S, (unsigned)((items + kMoveThreads - 1) / kMoveThreads));
-    cache_compact_rows_kernel<<<grid, kMoveThreads, 0, stream>>>(p);
+    // about 7 blocks per SM (what its registers hold) at once, each with some columns
+    long long each = ((long long)sms * 7 + p.c.S - 1) / p.c.S;
+    const long long most = (items + kMoveThreads - 1) / kMoveThreads;
+    if (each > most) each = most;
+    cache_compact_rows_kernel<<<dim3((unsigned)p.c.S, (unsigned)each), kMoveThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cache_compact_pages_kernel<<<(p.c.S + 3) / 4, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(cache_compact_pages_kernel, dim3((unsigned)((p.c.S + 3) / 4)), 128, stream, p);
 }
 
 }  // namespace gqa

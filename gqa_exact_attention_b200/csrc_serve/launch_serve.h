@@ -44,7 +44,7 @@ struct CompactParams {
 
 cudaError_t launch_resize(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_fork(const PlanParams& p, const Pools& pools, int sms, cudaStream_t stream);
-cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention
 struct ServeParams;

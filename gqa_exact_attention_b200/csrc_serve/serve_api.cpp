@@ -103,7 +103,7 @@ gqa_status check_requests(const int* a, bool need_a, const int* b, int n, const 
 
 gqa_status check_pools(const void* k, const void* v, int layers, long long row_bytes) {
     if (layers < 1 || row_bytes < 16 || row_bytes % 16 != 0 || row_bytes > (1ll << 24)) return GQA_ERR_SHAPE;
-    if ((long long)layers * row_bytes / 8 >= 65535ll * 128) return GQA_ERR_SHAPE;
+    if ((long long)layers * row_bytes >= (1ll << 31)) return GQA_ERR_SHAPE;  // 32-bit columns in the kernels
     if (!k || !v) return GQA_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16)) return GQA_ERR_ALIGN;
     return GQA_OK;
@@ -266,24 +266,24 @@ void fill_common(gqa::ServeParams* p, int B, int Hq, int Hk, float scale, long l
     p->inject_stall = std::getenv("GQA_FAULT_INJECT_STALL") != nullptr ? 1 : 0;
 }
 
-// The ranges schedule: every CTA slot gets an equal share of all key blocks.
-gqa_status run_ranges(gqa::ServeParams* p, int dev, int sms, int d, int nt, cudaStream_t stream) {
+// The ranges schedule: every CTA slot gets an equal share of all key blocks.  Units of at most
+// kWholeBlocks blocks are not split: a CTA that walks one alone is done before the partials of
+// several would be written and joined, and needs no scratch.
+gqa_status run_ranges(gqa::ServeParams* p, int dev, int sms, int d, int nt, long long most_keys, cudaStream_t stream) {
+    constexpr int kWholeBlocks = 4;
     const int grid = sms * gqa::serve_ctas_per_sm(nt);
-    const size_t rows = (size_t)2 * grid * nt * gqa::kServeBlockM;
+    p->whole = most_keys <= kWholeBlocks * gqa::kServeBlockN ? 1 : 0;
+    p->min_blocks = p->whole ? 1 : 2;
     const bool prefix = p->B > gqa::kServeOwnPrefix;
+    if (p->whole && !prefix) return launched(gqa::launch_serve(*p, d, nt, grid, stream));
+    const size_t rows = (size_t)2 * grid * nt * gqa::kServeBlockM;
     using W = Workspace;
-    W ws(dev, W::size_of<float>(rows * d) + W::size_of<float>(rows) + W::size_of<int>(2 * grid) +
+    W ws(dev, W::size_of<float>(rows * d) + W::size_of<float>(rows) +
                   (prefix ? W::size_of<long long>((size_t)p->B + 1) : 0), stream);
     if (!ws.ok()) return GQA_ERR_ALLOC;
     p->part_o = ws.take<float>(rows * d);
     p->part_lse = ws.take<float>(rows);
-    p->part_count = ws.take<int>(2 * grid);
     p->pre = prefix ? ws.take<long long>((size_t)p->B + 1) : nullptr;
-    p->min_blocks = 2;
-    if (cudaMemsetAsync(p->part_count, 0, 2 * grid * sizeof(int), stream) != cudaSuccess) {
-        cudaGetLastError();
-        return GQA_ERR_CUDA;
-    }
     return launched(gqa::launch_serve(*p, d, nt, grid, stream));
 }
 
@@ -378,7 +378,7 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (tiles >= 2 && units >= 3ll * info.sms) return run_list(&p, dev, info.sms, d, s);
     p.kv_shared = (tiles > 1 || !p.pack) ? 1 : 0;
-    return run_ranges(&p, dev, info.sms, d, 1, s);
+    return run_ranges(&p, dev, info.sms, d, 1, total_k, s);
 }
 
 gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -443,7 +443,7 @@ gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_c
             return GQA_ERR_CUDA;
     }
     p.kv_shared = (tiles > nt || !p.pack) ? 1 : 0;
-    return run_ranges(&p, dev, info.sms, d, nt, static_cast<cudaStream_t>(stream));
+    return run_ranges(&p, dev, info.sms, d, nt, p.cap, static_cast<cudaStream_t>(stream));
 }
 
 gqa_status gqa_cache_resize(int* block_table, int* cache_seqlens, int* page_refs, int S,
@@ -508,7 +508,7 @@ gqa_status gqa_cache_compact(void* k_pages, void* v_pages, int layers, long long
     p.tree_lens = tree_lens;
     p.T = T;
     p.status = status;
-    return launched(gqa::launch_compact(p, static_cast<cudaStream_t>(stream)));
+    return launched(gqa::launch_compact(p, info.sms, static_cast<cudaStream_t>(stream)));
 }
 
 gqa_status gqa_serve_device_status(int reset) {

@@ -4,7 +4,7 @@
 // The row softmax in one pass: S = Q K^T of a 128-row tile and a 128-key block in tensor
 // memory, P = 2^(c s - m) in bf16 over it (c = scale log2 e; the row sums keep the unrounded
 // P in fp32), O += P V in tensor memory.  m is a reference maximum that moves only when a
-// block's maximum leaves [m - 64, m + 8], by integers, so that rescaling is exact.
+// block's maximum passes it by more than 8 octaves.
 //
 // Work comes in units: a group of NT tiles of one sequence and head (or head group, whose g
 // query heads fold into a tile's rows).  Two schedules over them:
@@ -12,8 +12,8 @@
 //    CTAs in alternating direction; bound by the tensor pipe.
 //  - ranges (few rows over many keys: trees, short prompts): all units' key blocks in one
 //    row, cut into one equal range per CTA.  Every CTA streams the same number of blocks
-//    whatever the lengths are; a unit that several CTAs share leaves fp32 partials, which the
-//    CTA that finishes last joins, in the order of the keys.  Bound by HBM.
+//    whatever the lengths are; a unit that several CTAs share leaves fp32 partials, which a
+//    second kernel joins in the order of the keys.  Bound by HBM.
 // Roles:
 //   warpgroup 0, warp 0   TMA producer: Q tiles once per unit, then a ring of K/V blocks.
 //   warpgroup 0, warp 1   MMA issuer (one elected lane).
@@ -75,7 +75,7 @@ struct Cfg {
     // d = 64 with two tiles: S and O take 384 of 512 columns, so P has columns of its own and
     // the next block's S is computed while this block's softmax runs
     static constexpr bool kSepP = (HD == 64 && NT == 2);
-    static constexpr int kNumBars = 2 * kSlots + 8 * NT + 6 + (kSepP ? 2 * NT : 0) + 2 * kSegs;
+    static constexpr int kNumBars = 2 * kSlots + 8 * NT + 4 + (kSepP ? 2 * NT : 0) + 2 * kSegs;
     // warps that read the pieces the scheduler posts: producer, MMA, clearing, softmax, epilogue
     static constexpr int kReaders = 3 + 4 * NT + (kEpilogueWG ? 4 : 0);
     static constexpr int kStatsBytes = kEpilogueWG ? 2 * NT * 2 * 128 * 4 : 0;  // (m, l), 2 buffers
@@ -84,6 +84,13 @@ struct Cfg {
     static constexpr int kSmemBytes = 1024 /* alignment slack */ + NT * kTileBytes + kSlots * kTileBytes +
                                       kOStageBytes + 8 * kNumBars + kStatsBytes + kPreBytes + 16 + kSegs * 128;
     static_assert(kSmemBytes * kCtasPerSm + 1024 * kCtasPerSm <= 233472, "shared memory per SM");
+    // of each 16 exponential pairs of an unmasked 32-key chunk, this many take the polynomial
+    // instead of the special-function unit
+#ifdef SERVE_POLY
+    static constexpr int kPolyPairs = SERVE_POLY;
+#else
+    static constexpr int kPolyPairs = HD == 128 ? 0 : 3;
+#endif
     static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, false);
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, HD, true);
     __device__ static uint64_t sdesc(uint32_t saddr, uint32_t lbo) { return sdesc_sw128(saddr, lbo, 1024); }
@@ -96,6 +103,28 @@ struct Cfg {
     }
     static constexpr int kPAfterO = NT * HD;  // separate P lies this many columns past O
 };
+
+// 2^x on two lanes at once on the FMA pipe: x = j + f with j the nearest integer, 2^f by the
+// degree-4 polynomial with constant term 1 that has the least relative error on [-1/2, 1/2]
+// (2.8e-6: below the sums' and far below bf16's rounding), and j added to the exponent.  x is at
+// most 8 here; below -126 it counts as -126.
+__device__ __forceinline__ void exp2_poly4(float x0, float x1, float& y0, float& y1) {
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves j in the low bits
+    constexpr float c1 = 0.6931241750717163f, c2 = 0.24024099111557007f, c3 = 0.055906426161527634f,
+                    c4 = 0.009582853876054287f;
+    x0 = fmaxf(x0, -126.f);
+    x1 = fmaxf(x1, -126.f);
+    float t0, t1, r0, r1, f0, f1, q0, q1;
+    add2(x0, x1, kRound, kRound, t0, t1);
+    add2(t0, t1, -kRound, -kRound, r0, r1);
+    add2(x0, x1, -r0, -r1, f0, f1);
+    fma2(f0, f1, c4, c4, c3, c3, q0, q1);
+    fma2(q0, q1, f0, f1, c2, c2, q0, q1);
+    fma2(q0, q1, f0, f1, c1, c1, q0, q1);
+    fma2(q0, q1, f0, f1, 1.f, 1.f, q0, q1);
+    y0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+    y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+}
 
 template <uint32_t R>
 __device__ __forceinline__ void regs_inc() {
@@ -131,9 +160,11 @@ __device__ __forceinline__ Seq seq_of(const ServeParams& p, int b) {
     return s;
 }
 
-// The key blocks that a unit counts in the ranges schedule; a unit without keys counts one
-// (its rows are written all the same).
-__device__ __forceinline__ int unit_blocks(int sk) { return max((sk + kBlockN - 1) / kBlockN, 1); }
+// The steps that a unit counts in the ranges schedule: its key blocks (one without keys: its rows
+// are written all the same), or one where units are not split.
+__device__ __forceinline__ int unit_steps(const ServeParams& p, int sk) {
+    return p.whole ? 1 : max((sk + kBlockN - 1) / kBlockN, 1);
+}
 template <int NT>
 __device__ __forceinline__ int tile_groups(const ServeParams& p, int lq) {
     return (lq + NT * p.pos_per_tile - 1) / (NT * p.pos_per_tile);
@@ -147,10 +178,8 @@ struct Seg {
     int pos0[NT];  // first query position of tile t
     int n[NT];     // key blocks of tile t in this piece
     int kb_lo, nblk;
-    int parts;       // pieces of the unit (1: this is the whole unit)
-    int slot;        // where this piece's partials go
-    int first_slot;  // where the unit's first piece's are, and its count
-    int cta0;        // the first piece's CTA: piece i > 0 is in slot 2 (cta0 + i)
+    int parts;  // pieces of the unit (1: this is the whole unit)
+    int slot;   // where this piece's partials go
     // rows of V behind the last key in the last block: they are cleared before P V
     __device__ __forceinline__ bool dirty() const { return nblk > 0 && (kb_lo + nblk) * kBlockN > s.sk; }
 };
@@ -161,10 +190,63 @@ struct Walk {
     int ctas;                // CTAs that take part
     int b;
 };
-__device__ __forceinline__ long long range_start(const Walk& w, int cta) { return w.all * cta / w.ctas; }
+// floor(a * b / c): 64-bit division is slow, and rarely needed
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+    const long long ab = a * b;
+    if ((unsigned long long)ab < (1ull << 32) && c < (1ll << 32)) return (uint32_t)ab / (uint32_t)c;
+    return ab / c;
+}
+__device__ __forceinline__ long long range_start(const Walk& w, int cta) { return mul_div(w.all, cta, w.ctas); }
 __device__ __forceinline__ int cta_of(const Walk& w, long long x) {
-    // the last CTA whose range starts at or before x (no range is empty: ctas <= all)
-    return (int)(((x + 1) * w.ctas - 1) / w.all);
+    // the last CTA whose range starts at or before x, c < (x + 1) ctas / all (no range is empty:
+    // ctas <= all)
+    const long long a = (x + 1) * w.ctas - 1;
+    return (int)mul_div(a, 1, w.all);
+}
+__device__ __forceinline__ int ctas_of(const ServeParams& p, long long all, int grid) {
+    return (int)min((long long)grid, max(mul_div(all, 1, p.min_blocks), 1ll));
+}
+// the last sequence that starts at or before step x
+__device__ __forceinline__ int seq_at(const ServeParams& p, const long long* pre, long long x) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The unit that step x of sequence b belongs to, and how CTAs share it.
+struct UnitAt {
+    Seq s;
+    int hg, mt;
+    int blk, steps;  // x is its step blk of `steps`
+    int cta0;        // the CTA that begins it
+    int parts;       // CTAs that share it
+    int first_slot;  // where the first one's partials are; piece i > 0 is in slot 2 (cta0 + i)
+};
+template <int NT, int MODE>
+__device__ __forceinline__ UnitAt unit_at(const ServeParams& p, const long long* pre, const Walk& w, int b, long long x) {
+    UnitAt u;
+    u.s = seq_of<MODE>(p, b);
+    u.steps = unit_steps(p, u.s.sk);
+    const long long y = x - pre[b];
+    const int unit = (int)mul_div(y, 1, u.steps);
+    u.blk = (int)(y - (long long)unit * u.steps);
+    const int groups = tile_groups<NT>(p, u.s.lq);
+    u.hg = unit / groups;
+    u.mt = unit - u.hg * groups;
+    u.cta0 = 0;
+    u.parts = 1;
+    u.first_slot = 0;
+    if (!p.whole) {
+        const long long begin = x - u.blk;
+        u.cta0 = cta_of(w, begin);
+        u.parts = cta_of(w, begin + u.steps - 1) - u.cta0 + 1;
+        u.first_slot = 2 * u.cta0 + (range_start(w, u.cta0) == begin ? 0 : 1);
+    }
+    return u;
 }
 
 template <int NT, int MODE>
@@ -177,18 +259,11 @@ __device__ __forceinline__ Walk walk_begin(const ServeParams& p, const long long
         w.x_end = w.all;
     } else {
         w.all = pre[p.B];
-        const long long most = max(w.all / p.min_blocks, 1ll);
-        w.ctas = (int)min((long long)gridDim.x, most);
+        w.ctas = ctas_of(p, w.all, (int)gridDim.x);
         if ((int)blockIdx.x < w.ctas && w.all > 0) {
             w.x = w.x0 = range_start(w, blockIdx.x);
             w.x_end = range_start(w, blockIdx.x + 1);
-            int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before x
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (pre[mid] <= w.x) lo = mid;
-                else hi = mid - 1;
-            }
-            w.b = lo;
+            w.b = seq_at(p, pre, w.x);
         }
     }
     return w;
@@ -212,27 +287,20 @@ __device__ __forceinline__ bool next_seg(Walk& w, Seg<NT>& g, const ServeParams&
         g.kb_lo = 0;
         hi = 0x7fffffff;
         g.parts = 1;
-        g.slot = g.first_slot = g.cta0 = 0;
+        g.slot = 0;
         w.x += w.ctas;
     } else {
         while (w.x >= pre[w.b + 1]) ++w.b;
         g.b = w.b;
-        g.s = seq_of<MODE>(p, g.b);
-        const int nb = unit_blocks(g.s.sk);
-        const long long y = w.x - pre[w.b];
-        const int unit = (int)(y / nb);
-        const int blk = (int)(y - (long long)unit * nb);
-        const int len = (int)min((long long)(nb - blk), w.x_end - w.x);
-        const int groups = tile_groups<NT>(p, g.s.lq);
-        g.hg = unit / groups;
-        mt = unit - g.hg * groups;
-        g.kb_lo = blk;
-        hi = blk + len;
-        const long long begin = w.x - blk;
-        g.cta0 = cta_of(w, begin);
-        g.parts = cta_of(w, begin + nb - 1) - g.cta0 + 1;
+        const UnitAt u = unit_at<NT, MODE>(p, pre, w, g.b, w.x);
+        const int len = (int)min((long long)(u.steps - u.blk), w.x_end - w.x);
+        g.s = u.s;
+        g.hg = u.hg;
+        mt = u.mt;
+        g.kb_lo = p.whole ? 0 : u.blk;
+        hi = p.whole ? 0x7fffffff : u.blk + len;
+        g.parts = u.parts;
         g.slot = 2 * (int)blockIdx.x + (w.x == w.x0 ? 0 : 1);
-        g.first_slot = 2 * g.cta0 + (range_start(w, g.cta0) == begin ? 0 : 1);
         w.x += len;
     }
     g.kvh = p.pack ? g.hg : (int)fastdiv((uint32_t)g.hg, p.div_g);
@@ -380,45 +448,6 @@ __device__ __forceinline__ void write_piece(const ServeParams& p, uint32_t o_add
     else write_row<HD, NT, MODE, true>(p, o_addr, rm, g, t, row, has, idle, valid, m, l, o_empty_bar);
 }
 
-// Joins the parts of one row: with L_i = log2 sum of part i, M = max L_i and w_i = 2^(L_i - M),
-// O = sum w_i O_i / sum w_i and LSE = (M + log2 sum w_i) ln 2, in the order of the keys.
-template <int HD, int NT, int MODE>
-__device__ __forceinline__ void join_row(const ServeParams& p, const RowMap& rm, const Seg<NT>& g, int t, int row) {
-    auto slot_of = [&](int i) { return i == 0 ? g.first_slot : 2 * (g.cta0 + i); };
-    auto row_of = [&](int i) { return ((size_t)slot_of(i) * NT + t) * 128 + row; };
-    float M = -INFINITY;
-    for (int i = 0; i < g.parts; ++i) M = fmaxf(M, __ldcg(p.part_lse + row_of(i)));
-    float sum = 0.f;
-    if (M > -INFINITY)
-        for (int i = 0; i < g.parts; ++i) sum += ex2_approx(__ldcg(p.part_lse + row_of(i)) - M);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const size_t at = out_row<MODE>(p, g.b, g.s, rm) * HD;
-    // 8 columns at a time: the epilogue warpgroup has few registers
-#pragma unroll 1
-    for (int col = 0; col < HD; col += 8) {
-        float f[8] = {};
-        for (int i = 0; i < g.parts; ++i) {
-            const float li = __ldcg(p.part_lse + row_of(i));
-            if (!(li > -INFINITY)) continue;  // no keys in this part
-            const float w = ex2_approx(li - M);
-            const float4* src = reinterpret_cast<const float4*>(p.part_o + row_of(i) * HD + col);
-            const float4 x = __ldcg(src), y = __ldcg(src + 1);
-            f[0] += w * x.x, f[1] += w * x.y, f[2] += w * x.z, f[3] += w * x.w;
-            f[4] += w * y.x, f[5] += w * y.y, f[6] += w * y.z, f[7] += w * y.w;
-        }
-        if (p.out_bf16 != nullptr) {
-            *reinterpret_cast<uint4*>(p.out_bf16 + at + col) =
-                make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                           pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
-        } else {
-            float4* dst = reinterpret_cast<float4*>(p.out + at + col);
-            dst[0] = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-            dst[1] = make_float4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-        }
-    }
-    p.lse[lse_row<MODE>(p, g.b, g.s, rm)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
-}
-
 // Paged KV: the block-table entries of one sequence, cached in the producer warp's
 // registers 32 at a time (lane i holds entry base + i), with the next 32 already loaded
 // (lane i of w1 holds base + 32 + i) so that moving on does not wait for memory.
@@ -486,21 +515,6 @@ __device__ __forceinline__ uint32_t tree_word(const int* row, int i, int nodes) 
     return left >= 32 ? w : w & ((1u << left) - 1u);
 }
 
-// Counts a written part of a unit; true, for the whole epilogue warpgroup, in the CTA that wrote
-// the last.  All 128 threads call it.
-template <int NT>
-__device__ __forceinline__ bool last_part(const ServeParams& p, const Seg<NT>& g, bool first_thread, uint32_t bar,
-                                          volatile uint32_t* flag) {
-    __threadfence();  // the part is visible before it is counted
-    named_bar_sync(bar, 128);
-    if (first_thread) *flag = atomicAdd(p.part_count + g.first_slot, 1) == g.parts - 1 ? 1u : 0u;
-    named_bar_sync(bar, 128);
-    const bool last = *flag != 0u;
-    named_bar_sync(bar, 128);  // the flag may be written again
-    __threadfence();
-    return last;
-}
-
 // pre[b] = key blocks of all units of the sequences before b, by all threads of a block; the
 // caller synchronises afterwards.
 template <int NT, int MODE, int THREADS>
@@ -513,7 +527,7 @@ __device__ void block_prefix(const ServeParams& p, long long* pre) {
         long long x = 0;
         if (b < p.B) {
             const Seq s = seq_of<MODE>(p, b);
-            x = (long long)p.n_hg * tile_groups<NT>(p, s.lq) * unit_blocks(s.sk);
+            x = (long long)p.n_hg * tile_groups<NT>(p, s.lq) * unit_steps(p, s.sk);
         }
         long long incl = x;
 #pragma unroll
@@ -557,8 +571,6 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(stats) + C::kStatsBytes);
     const uint32_t bar0 = smem_u32(bars);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    // [0]: the join decision, passed from one thread to its warpgroup
-    volatile uint32_t* join_flag = tmem_slot + 2;
     // blocks before each sequence (the ranges schedule)
     long long* own_pre = reinterpret_cast<long long*>(tmem_slot + 4);
     Seg<NT>* segs = reinterpret_cast<Seg<NT>*>(own_pre + kServeOwnPrefix + 1);
@@ -584,14 +596,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
     const uint32_t stall_bar = bar0 + 8u * (2 * C::kSlots + 8 * NT + 1);
     // a V block with rows behind a sequence's last key has landed (MMA -> warp 2), and they are
     // cleared (warp 2 -> MMA).  Warp 2 does not follow the ring by itself: it would miss phases.
-    const uint32_t v_dirty = bar0 + 8u * (2 * C::kSlots + 8 * NT + 5);
+    const uint32_t v_dirty = bar0 + 8u * (2 * C::kSlots + 8 * NT + 3);
     const uint32_t v_clean = bar0 + 8u * (2 * C::kSlots + 8 * NT + 2);
-    // NT = 1: a part is written (128 threads), and whether it was the unit's last one is known
-    [[maybe_unused]] const uint32_t part_written = bar0 + 8u * (2 * C::kSlots + 8 * NT + 3);
-    [[maybe_unused]] const uint32_t part_counted = bar0 + 8u * (2 * C::kSlots + 8 * NT + 4);
     // separate P (kSepP): S_t read into registers (softmax -> MMA), P_t.V done (MMA -> softmax)
-    [[maybe_unused]] auto s_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 8 * NT + 6 + t); };
-    [[maybe_unused]] auto p_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 8 * NT + 6 + NT + t); };
+    [[maybe_unused]] auto s_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 8 * NT + 4 + t); };
+    [[maybe_unused]] auto p_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 8 * NT + 4 + NT + t); };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -616,8 +625,6 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
         mbar_init(stall_bar, 1);
         mbar_init(v_dirty, 1);
         mbar_init(v_clean, 1);
-        mbar_init(part_written, 128);
-        mbar_init(part_counted, 1);
         for (uint32_t i = 0; i < kSegs; ++i) {
             mbar_init(seg_full(i), 1);
             mbar_init(seg_empty(i), C::kReaders);
@@ -643,6 +650,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
     }
     const long long* pre = p.pre;
     if constexpr (kRanges) {
+        // the joining kernel's CTAs may come as these leave; it waits for all of them by itself
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         // the blocks of each sequence's units, summed up by every CTA for itself
         if (pre == nullptr) {
             block_prefix<NT, MODE, C::kThreads>(p, own_pre);
@@ -1123,28 +1132,6 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
         const float fill = (c >= 0.f) ? -INFINITY : INFINITY;  // masked keys drop out of the extremum
         uint32_t sn = 0, stn = 0, sn_o = 0;
         bool ok = true;
-        // The piece is written: it is counted, and the CTA that wrote a unit's last one joins the
-        // parts.  The warps wait for one another on bounded barriers here, as everywhere.
-        uint32_t jn = 0;
-        [[maybe_unused]] auto finish = [&](const Seg<NT>& g, const RowMap& rm, int row) {
-            if constexpr (!C::kEpilogueWG && kRanges) {
-                if (g.parts == 1) return;
-                __threadfence();  // the part is visible before it is counted
-                mbar_arrive(part_written);
-                if (quarter == 0) {
-                    ok = __all_sync(0xffffffffu, wait_bounded(part_written, jn & 1u, abort_flag, p));
-                    if (ok && lane == 0) {
-                        *join_flag = atomicAdd(p.part_count + g.first_slot, 1) == g.parts - 1 ? 1u : 0u;
-                        mbar_arrive(part_counted);
-                    }
-                }
-                if (ok) ok = __all_sync(0xffffffffu, wait_bounded(part_counted, jn & 1u, abort_flag, p));
-                ++jn;
-                if (!ok || *join_flag == 0u) return;
-                __threadfence();
-                if (rm.ok) join_row<HD, NT, MODE>(p, rm, g, 0, row);
-            }
-        };
 
         for (uint32_t si = 0; ok; ++si) {
             const Seg<NT>* const piece = next_piece(si, ok);
@@ -1156,7 +1143,6 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
             if (n_t == 0) {
                 if constexpr (!C::kEpilogueWG) {
                     write_piece<HD, NT, MODE>(p, o_addr, rm, g, t, row, false, false, valid, -INFINITY, 0.f, 0u);
-                    finish(g, rm, row);
                 }
                 done_piece(si);
                 continue;
@@ -1203,14 +1189,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                     ++sn_o;
                     tc_fence_after();
                     write_piece<HD, NT, MODE>(p, o_addr, rm, g, t, row, true, true, valid, kNegInf, 0.f, o_empty(t));
-                    finish(g, rm, row);
                 }
                 done_piece(si);
                 continue;
             }
 
             const int kb_lo = g.kb_lo, nodes = g.s.nodes;
-            float m = 0.f;  // reference max of c*s (log2 units), see below
+            float m = kNegInf;  // reference max of c*s (log2 units), see below
             float l = 0.f;
             for (int it = 0; it < n_t; ++it) {
                 ok = __all_sync(0xffffffffu, wait_bounded(s_full(t), sn & 1u, abort_flag, p));
@@ -1314,16 +1299,16 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                     e[0] = extremum([](float x, float y, float z) { return min3(x, y, z); },
                                     [](float x, float y) { return fminf(x, y); });
                 const float mx = nothing ? kNegInf : (c == 0.f ? 0.f : e[0] * c);
-                // Reference max m (log2 units): it starts at 0, and moves only when a block's max
-                // leaves [m - 64, m + 8] (down only while nothing has been summed yet), to the
-                // block max rounded up to an integer: rescaling multiplies by powers of two.
-                const bool grow = mx > m + 8.0f || (l == 0.f && mx > kNegInf && mx < m - 64.f);
+                // Reference max m (log2 units): the max of the row's first block with a key, exactly
+                // (so that the largest weight is 1 and a row with one key gives its value back), then
+                // moved only when a block's max passes m + 8, which keeps every p <= 256 and spares
+                // most rows the rescaling of O.
+                const bool grow = mx > m + 8.0f || (l == 0.f && mx > m);
                 float alpha = 1.f;
                 if (grow) {
-                    const float m_new = ceilf(mx);
-                    alpha = (l == 0.f) ? 0.f : ex2_approx(m - m_new);  // nothing summed: O is 0
+                    alpha = (l == 0.f) ? 0.f : ex2_approx(m - mx);  // nothing summed: O is 0
                     l *= alpha;
-                    m = m_new;
+                    m = mx;
                 }
                 // P = 2^(c*s - m) as bf16, written over S in TMEM (S is in registers).  A
                 // disallowed key gets the exponent -inf, i.e. p = 0, for any sign of c.
@@ -1332,6 +1317,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 // One 32-key chunk: P = 2^(c s - m) as 16 columns of bf16 pairs; with kSelect, keys
                 // that the row does not see get the exponent -inf (p = 0 for either sign of c).
                 // bf16 is the matrix unit's input: the sum keeps the unrounded p.
+                // the pairs of a chunk that take the polynomial, spread over the chunk
+                auto use_poly = [](int ch, int i) { return ((i * 5 + ch * 3) & 15) < C::kPolyPairs; };
                 auto exp_chunk = [&](auto select_c, int ch) {
                     constexpr bool kSelect = decltype(select_c)::value;
                     uint32_t pk[16];
@@ -1344,7 +1331,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                             x0 = sees(ch, 2 * i) ? x0 : kNegInf;
                             x1 = sees(ch, 2 * i + 1) ? x1 : kNegInf;
                         }
-                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                        float p0, p1;
+                        if (!kSelect && use_poly(ch, i)) {
+                            exp2_poly4(x0, x1, p0, p1);
+                        } else {
+                            p0 = ex2_approx(x0);
+                            p1 = ex2_approx(x1);
+                        }
                         add2(ls0, ls1, p0, p1, ls0, ls1);
                         pk[i] = pack_bf16x2(p0, p1);
                     }
@@ -1413,7 +1406,6 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 ++sn_o;
                 tc_fence_after();
                 write_piece<HD, NT, MODE>(p, o_addr, rm, g, t, row, true, false, valid, m, l, o_empty(t));
-                finish(g, rm, row);
             }
             done_piece(si);
         }
@@ -1550,16 +1542,6 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 }
                 if (rm.ok) p.lse[lse_row<MODE>(p, g.b, g.s, rm)] = lse_v;
             }
-            if constexpr (kRanges) {
-                if (ok && g.parts > 1 && last_part(p, g, issuer, kEpiBar, join_flag)) {
-#pragma unroll 1
-                    for (int t = 0; t < NT; ++t) {
-                        if (pick<NT>(g.pos0, t) >= g.s.lq) continue;
-                        const RowMap rm = row_map(p, g.s.lq, pick<NT>(g.pos0, t), g.hg, row);
-                        if (rm.ok) join_row<HD, NT, MODE>(p, rm, g, t, row);
-                    }
-                }
-            }
             done_piece(si);
         }
         if (issuer) bulk_wait_all();
@@ -1571,6 +1553,119 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc<C::kTmemCols>(tmem);
+    }
+}
+
+// ---------------------------------------------------------------- joining the parts
+// A unit is shared where a CTA's range begins inside it: boundary c is the begin of CTA c's range.
+// The blocks of boundary c (blockIdx.x = c - 1) join a share of its unit's rows, 1 of parts - 1,
+// so that units in many parts are spread over as many blocks.  With L_i = log2 of part i's sum,
+// M = max L_i and w_i = 2^(L_i - M), O = sum w_i O_i / sum w_i and LSE = (M + log2 sum w_i) ln 2,
+// in the order of the keys.  The partials come from L2, and the latency of those reads is what
+// it costs: a warp takes eight rows at once (lanes = 8 rows x 4 parts for the L_i, then 4 or 2
+// columns of each row), so that each step has eight loads in flight.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 2;  // per boundary
+template <int HD, int NT, int MODE>
+__global__ void __launch_bounds__(kJoinThreads) serve_join_kernel(const __grid_constant__ ServeParams p) {
+    __shared__ long long own_pre[kServeOwnPrefix + 1];
+    const long long* pre = p.pre;
+    if (pre == nullptr) {
+        block_prefix<NT, MODE, kJoinThreads>(p, own_pre);
+        pre = own_pre;
+        __syncthreads();
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+    const int c = (int)blockIdx.x + 1;
+    Walk w{};
+    w.all = pre[p.B];
+    w.ctas = ctas_of(p, w.all, (int)gridDim.x + 1);
+    bool mine = c < w.ctas;
+    UnitAt u{};
+    int b = 0;
+    if (mine) {
+        const long long x = range_start(w, c);
+        b = seq_at(p, pre, x);
+        u = unit_at<NT, MODE>(p, pre, w, b, x);
+        mine = u.blk > 0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!mine) return;
+    constexpr int kRows = NT * 128;
+    const int lane = threadIdx.x & 31;
+    const int shares = (u.parts - 1) * kJoinBlocks, share = (c - u.cta0 - 1) * kJoinBlocks + (int)blockIdx.y;
+    const int r_end = (int)((long long)kRows * (share + 1) / shares);
+    auto row_of = [&](int i, int r) { return (size_t)(i == 0 ? u.first_slot : 2 * (u.cta0 + i)) * kRows + r; };
+    constexpr int kPer = HD / 32;
+    const int mine4 = lane & 3;
+    for (int r0 = (int)((long long)kRows * share / shares) + (threadIdx.x >> 5) * 8; r0 < r_end; r0 += kJoinThreads / 4) {
+        // lane = (row r0 + lane / 4, every fourth part)
+        const int rl = r0 + (lane >> 2);
+        const RowMap rm = row_map(p, u.s.lq, (u.mt * NT + rl / 128) * p.pos_per_tile, u.hg, rl % 128);
+        const bool ok = rl < r_end && rm.ok;
+        float M = -INFINITY;
+        if (ok)
+            for (int i = mine4; i < u.parts; i += 4) M = fmaxf(M, __ldcg(p.part_lse + row_of(i, rl)));
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+        float acc[8][kPer] = {}, sum = 0.f;
+        for (int i0 = 0; i0 < u.parts; i0 += 4) {
+            const float li = ok && i0 + mine4 < u.parts ? __ldcg(p.part_lse + row_of(i0 + mine4, rl)) : -INFINITY;
+            const float wl = li > -INFINITY ? ex2_approx(li - M) : 0.f;  // 0: no keys in this part
+            sum += wl;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (i0 + j >= u.parts) break;
+                float v[8][kPer], wi[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    wi[e] = __shfl_sync(0xffffffffu, wl, e * 4 + j);
+                    const float* src = p.part_o + row_of(i0 + j, r0 + e) * HD + lane * kPer;
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x) v[e][x] = 0.f;
+                    if (wi[e] != 0.f) {  // (else its rows were not written)
+                        if constexpr (kPer == 4) {
+                            const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+                            v[e][0] = t.x, v[e][1] = t.y, v[e][2] = t.z, v[e][3] = t.w;
+                        } else {
+                            const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+                            v[e][0] = t.x, v[e][1] = t.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x) acc[e][x] += wi[e] * v[e][x];
+            }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (ok && mine4 == 0)
+            p.lse[lse_row<MODE>(p, b, u.s, rm)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+        const float inv_l = sum > 0.f ? 1.f / sum : 0.f;
+        const long long at_l = ok ? (long long)out_row<MODE>(p, b, u.s, rm) * HD : -1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float inv = __shfl_sync(0xffffffffu, inv_l, e * 4);
+            const long long row = __shfl_sync(0xffffffffu, at_l, e * 4);
+            if (row < 0) continue;
+            const size_t at = (size_t)row + lane * kPer;
+            if (p.out_bf16 != nullptr) {
+                if constexpr (kPer == 4)
+                    *reinterpret_cast<uint2*>(p.out_bf16 + at) = make_uint2(
+                        pack_bf16x2(acc[e][0] * inv, acc[e][1] * inv), pack_bf16x2(acc[e][2] * inv, acc[e][3] * inv));
+                else
+                    *reinterpret_cast<uint32_t*>(p.out_bf16 + at) = pack_bf16x2(acc[e][0] * inv, acc[e][1] * inv);
+            } else {
+                if constexpr (kPer == 4)
+                    *reinterpret_cast<float4*>(p.out + at) =
+                        make_float4(acc[e][0] * inv, acc[e][1] * inv, acc[e][2] * inv, acc[e][3] * inv);
+                else
+                    *reinterpret_cast<float2*>(p.out + at) = make_float2(acc[e][0] * inv, acc[e][1] * inv);
+            }
+        }
     }
 }
 
@@ -1688,7 +1783,23 @@ cudaError_t launch_t(const ServeParams& p, int grid, cudaStream_t stream) {
             serve_prefix_kernel<NT, MODE><<<1, 1024, 0, stream>>>(p, const_cast<long long*>(p.pre));
     }
     serve_fwd_kernel<HD, NT, MODE><<<grid, C::kThreads, C::kSmemBytes, stream>>>(p);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if constexpr (MODE != kVarlenList) {
+        if (e == cudaSuccess && !p.whole && grid > 1) {
+            // launched while the attention still runs (programmatic dependent launch)
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)grid - 1, kJoinBlocks);
+            cfg.blockDim = dim3(kJoinThreads);
+            cfg.stream = stream;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, serve_join_kernel<HD, NT, MODE>, p);
+        }
+    }
+    return e;
 }
 
 }  // namespace

@@ -51,10 +51,10 @@ struct ServeParams {
     const int2* list;         // (sequence, tile group), heaviest first within a window
     const int* list_len;      // its entries
     const long long* pre;     // [B + 1], NULL: summed up in the kernel
+    int whole;                // units are not split (no partials)
     int min_blocks;           // a CTA's range holds at least this many blocks (if there are)
     float* part_o;            // [2 * grid][NT][128][d]
     float* part_lse;          // [2 * grid][NT][128], log2 units
-    int* part_count;          // [2 * grid], zero: parts of a unit that are done
 
     int kv_shared;  // K/V blocks are read by several units: ask L2 to keep them
     long long timeout_ns, drain_ns;
