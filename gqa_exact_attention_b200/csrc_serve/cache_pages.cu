@@ -247,22 +247,33 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         free_before = __shfl_sync(0xffffffffu, incl, 31) - mine;
         if (tid == 0) cta_free = (int)total;
         cluster.sync();
-        for (int r = 0; r < kClusterCtas; ++r) {
-            const int x = *cluster.map_shared_rank(&cta_free, r);
-            if (r < rank) free_before += x;
-            free_all += x;
-        }
+        // (each of the first lanes reads one block's count)
+        int x = lane < kClusterCtas ? *cluster.map_shared_rank(&cta_free, lane) : 0;
+        free_all = __reduce_add_sync(0xffffffffu, x);
+        free_before += __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
 
         // ---- 4. each warp hands out its own free pages
         for (int at = p_lo; at < p_hi && free_before < needed; at += kFew * 32) {
-            const unsigned m = at == p_lo ? first_mask : free_mask(at);
-#pragma unroll 1
-            for (int e = 0; e < kFew && free_before < needed; ++e) {
-                const bool is_free = (m >> e) & 1u;
-                const unsigned ball = __ballot_sync(0xffffffffu, is_free);
-                const int r = free_before + __popc(ball & ((1u << lane) - 1u));
-                free_before += __popc(ball);
-                if (is_free && r < needed) {
+            unsigned m = at == p_lo ? first_mask : free_mask(at);
+            // lane e keeps group e's free lanes, and how many are free in the groups before
+            unsigned group = 0;
+#pragma unroll
+            for (int e = 0; e < kFew; ++e) {
+                const unsigned ball = __ballot_sync(0xffffffffu, (m >> e) & 1u);
+                if (lane == e) group = ball;
+            }
+            int upto_group = __popc(group);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto_group, o);
+                if (lane >= o) upto_group += y;
+            }
+            const int in_group = upto_group - __popc(group);
+            while (__any_sync(0xffffffffu, m != 0u)) {  // every lane's next page
+                const int e = m != 0u ? __ffs(m) - 1 : 0;
+                const unsigned others = __shfl_sync(0xffffffffu, group, e);
+                const int r = free_before + __shfl_sync(0xffffffffu, in_group, e) + __popc(others & ((1u << lane) - 1u));
+                if (m != 0u && r < needed) {
                     int lo = 0, hi = n - 1;  // the first request with upto > r
                     while (lo < hi) {
                         const int mid = (lo + hi) >> 1;
@@ -276,7 +287,9 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
                         c.refs[page] = 1;
                     }
                 }
+                m &= m - 1u;
             }
+            free_before += __shfl_sync(0xffffffffu, upto_group, 31);
         }
     }
 

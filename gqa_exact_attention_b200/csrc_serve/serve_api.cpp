@@ -278,11 +278,12 @@ gqa_status run_ranges(gqa::ServeParams* p, int dev, int sms, int d, int nt, long
     if (p->whole && !prefix) return launched(gqa::launch_serve(*p, d, nt, grid, stream));
     const size_t rows = (size_t)2 * grid * nt * gqa::kServeBlockM;
     using W = Workspace;
-    W ws(dev, W::size_of<float>(rows * d) + W::size_of<float>(rows) +
+    W ws(dev, W::size_of<float>(rows * d) + W::size_of<float>(rows) + W::size_of<gqa::ServeBound>(grid) +
                   (prefix ? W::size_of<long long>((size_t)p->B + 1) : 0), stream);
     if (!ws.ok()) return GQA_ERR_ALLOC;
     p->part_o = ws.take<float>(rows * d);
     p->part_lse = ws.take<float>(rows);
+    p->bounds = ws.take<gqa::ServeBound>(grid);
     p->pre = prefix ? ws.take<long long>((size_t)p->B + 1) : nullptr;
     return launched(gqa::launch_serve(*p, d, nt, grid, stream));
 }

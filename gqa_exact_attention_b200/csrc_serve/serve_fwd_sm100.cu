@@ -189,6 +189,7 @@ struct Walk {
     long long all;           // blocks or units in all
     int ctas;                // CTAs that take part
     int b;
+    ServeBound bound;  // ranges: the unit of the first piece
 };
 // floor(a * b / c): 64-bit division is slow, and rarely needed
 __device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
@@ -301,6 +302,8 @@ __device__ __forceinline__ bool next_seg(Walk& w, Seg<NT>& g, const ServeParams&
         hi = p.whole ? 0x7fffffff : u.blk + len;
         g.parts = u.parts;
         g.slot = 2 * (int)blockIdx.x + (w.x == w.x0 ? 0 : 1);
+        if (w.x == w.x0)
+            w.bound = {g.b, u.hg, u.mt, u.s.q0, u.s.lq, u.cta0, u.blk > 0 ? u.parts : 0, u.first_slot};
         w.x += len;
     }
     g.kvh = p.pack ? g.hg : (int)fastdiv((uint32_t)g.hg, p.div_g);
@@ -1110,6 +1113,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 if (lane == 0) {
                     segs[si % kSegs] = g;
                     mbar_arrive(seg_full(si));
+                    if constexpr (kRanges) {
+                        // the unit that this CTA's range begins in, for the joining kernel
+                        if (si == 0 && !p.whole) p.bounds[blockIdx.x] = w.bound;
+                    }
                 }
                 __syncwarp();
             }
@@ -1562,65 +1569,49 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
 // so that units in many parts are spread over as many blocks.  With L_i = log2 of part i's sum,
 // M = max L_i and w_i = 2^(L_i - M), O = sum w_i O_i / sum w_i and LSE = (M + log2 sum w_i) ln 2,
 // in the order of the keys.  The partials come from L2, and the latency of those reads is what
-// it costs: a warp takes eight rows at once (lanes = 8 rows x 4 parts for the L_i, then 4 or 2
-// columns of each row), so that each step has eight loads in flight.
+// it costs: a warp takes four rows at once (lanes = 4 rows x 8 parts for the L_i, then 4 or 2
+// columns of each row) and all blocks are resident at once.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBlocks = 2;  // per boundary
+constexpr int kJoinRows = 4, kJoinLanes = 32 / kJoinRows;
 template <int HD, int NT, int MODE>
-__global__ void __launch_bounds__(kJoinThreads) serve_join_kernel(const __grid_constant__ ServeParams p) {
-    __shared__ long long own_pre[kServeOwnPrefix + 1];
-    const long long* pre = p.pre;
-    if (pre == nullptr) {
-        block_prefix<NT, MODE, kJoinThreads>(p, own_pre);
-        pre = own_pre;
-        __syncthreads();
-    } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-    }
-    const int c = (int)blockIdx.x + 1;
-    Walk w{};
-    w.all = pre[p.B];
-    w.ctas = ctas_of(p, w.all, (int)gridDim.x + 1);
-    bool mine = c < w.ctas;
-    UnitAt u{};
-    int b = 0;
-    if (mine) {
-        const long long x = range_start(w, c);
-        b = seq_at(p, pre, x);
-        u = unit_at<NT, MODE>(p, pre, w, b, x);
-        mine = u.blk > 0;
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
+__global__ void __launch_bounds__(kJoinThreads, 4) serve_join_kernel(const __grid_constant__ ServeParams p) {
     constexpr int kRows = NT * 128;
     const int lane = threadIdx.x & 31;
+    const int c = (int)blockIdx.x + 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ServeBound u = p.bounds[c];
+    if (u.parts == 0) return;
+    Seq s{};
+    s.q0 = u.q0;
+    s.lq = u.lq;
     const int shares = (u.parts - 1) * kJoinBlocks, share = (c - u.cta0 - 1) * kJoinBlocks + (int)blockIdx.y;
     const int r_end = (int)((long long)kRows * (share + 1) / shares);
     auto row_of = [&](int i, int r) { return (size_t)(i == 0 ? u.first_slot : 2 * (u.cta0 + i)) * kRows + r; };
     constexpr int kPer = HD / 32;
-    const int mine4 = lane & 3;
-    for (int r0 = (int)((long long)kRows * share / shares) + (threadIdx.x >> 5) * 8; r0 < r_end; r0 += kJoinThreads / 4) {
-        // lane = (row r0 + lane / 4, every fourth part)
-        const int rl = r0 + (lane >> 2);
-        const RowMap rm = row_map(p, u.s.lq, (u.mt * NT + rl / 128) * p.pos_per_tile, u.hg, rl % 128);
+    const int part = lane % kJoinLanes;
+    for (int r0 = (int)((long long)kRows * share / shares) + (threadIdx.x >> 5) * kJoinRows; r0 < r_end;
+         r0 += kJoinThreads / 32 * kJoinRows) {
+        const int rl = r0 + lane / kJoinLanes;  // this lane's row for the L_i
+        const RowMap rm = row_map(p, s.lq, (u.mt * NT + rl / 128) * p.pos_per_tile, u.hg, rl % 128);
         const bool ok = rl < r_end && rm.ok;
         float M = -INFINITY;
         if (ok)
-            for (int i = mine4; i < u.parts; i += 4) M = fmaxf(M, __ldcg(p.part_lse + row_of(i, rl)));
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
-        float acc[8][kPer] = {}, sum = 0.f;
-        for (int i0 = 0; i0 < u.parts; i0 += 4) {
-            const float li = ok && i0 + mine4 < u.parts ? __ldcg(p.part_lse + row_of(i0 + mine4, rl)) : -INFINITY;
+            for (int i = part; i < u.parts; i += kJoinLanes) M = fmaxf(M, __ldcg(p.part_lse + row_of(i, rl)));
+#pragma unroll
+        for (int o = 1; o < kJoinLanes; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float acc[kJoinRows][kPer] = {}, sum = 0.f;
+        for (int i0 = 0; i0 < u.parts; i0 += kJoinLanes) {
+            const float li = ok && i0 + part < u.parts ? __ldcg(p.part_lse + row_of(i0 + part, rl)) : -INFINITY;
             const float wl = li > -INFINITY ? ex2_approx(li - M) : 0.f;  // 0: no keys in this part
             sum += wl;
+            const int n = min(kJoinLanes, u.parts - i0);
+#pragma unroll 2
+            for (int j = 0; j < n; ++j) {
+                float v[kJoinRows][kPer], wi[kJoinRows];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (i0 + j >= u.parts) break;
-                float v[8][kPer], wi[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    wi[e] = __shfl_sync(0xffffffffu, wl, e * 4 + j);
+                for (int e = 0; e < kJoinRows; ++e) {
+                    wi[e] = __shfl_sync(0xffffffffu, wl, e * kJoinLanes + j);
                     const float* src = p.part_o + row_of(i0 + j, r0 + e) * HD + lane * kPer;
 #pragma unroll
                     for (int x = 0; x < kPer; ++x) v[e][x] = 0.f;
@@ -1635,21 +1626,21 @@ __global__ void __launch_bounds__(kJoinThreads) serve_join_kernel(const __grid_c
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < kJoinRows; ++e)
 #pragma unroll
                     for (int x = 0; x < kPer; ++x) acc[e][x] += wi[e] * v[e][x];
             }
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (ok && mine4 == 0)
-            p.lse[lse_row<MODE>(p, b, u.s, rm)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
-        const float inv_l = sum > 0.f ? 1.f / sum : 0.f;
-        const long long at_l = ok ? (long long)out_row<MODE>(p, b, u.s, rm) * HD : -1;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float inv = __shfl_sync(0xffffffffu, inv_l, e * 4);
-            const long long row = __shfl_sync(0xffffffffu, at_l, e * 4);
+        for (int o = 1; o < kJoinLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (ok && part == 0)
+            p.lse[lse_row<MODE>(p, u.b, s, rm)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+        const float inv_l = sum > 0.f ? 1.f / sum : 0.f;
+        const long long at_l = ok ? (long long)out_row<MODE>(p, u.b, s, rm) * HD : -1;
+#pragma unroll
+        for (int e = 0; e < kJoinRows; ++e) {
+            const float inv = __shfl_sync(0xffffffffu, inv_l, e * kJoinLanes);
+            const long long row = __shfl_sync(0xffffffffu, at_l, e * kJoinLanes);
             if (row < 0) continue;
             const size_t at = (size_t)row + lane * kPer;
             if (p.out_bf16 != nullptr) {

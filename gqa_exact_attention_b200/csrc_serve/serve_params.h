@@ -14,6 +14,15 @@ constexpr int kServeBlockN = 128;  // keys of one K/V block
 // in front of the attention writes the sums to global memory
 constexpr int kServeOwnPrefix = 1024;
 
+// The unit that a CTA's range begins in, when it begins inside it (else parts is 0).
+struct ServeBound {
+    int b, hg, mt;
+    int q0, lq;      // its sequence's first query row and queries
+    int cta0;        // the CTA that begins it
+    int parts;       // CTAs that share it
+    int first_slot;  // where the first one's partials are; piece i > 0 is in slot 2 (cta0 + i)
+};
+
 struct ServeParams {
     CUtensorMap tm_q;  // varlen: q as (d, Hq, total_q, 1); tree: (d, Hq, T, B)
     CUtensorMap tm_k;  // varlen: (d, Hk, total_k, 1); tree: (d, Hk, Sk, B) or the page pool
@@ -55,6 +64,7 @@ struct ServeParams {
     int min_blocks;           // a CTA's range holds at least this many blocks (if there are)
     float* part_o;            // [2 * grid][NT][128][d]
     float* part_lse;          // [2 * grid][NT][128], log2 units
+    ServeBound* bounds;       // [grid]
 
     int kv_shared;  // K/V blocks are read by several units: ask L2 to keep them
     long long timeout_ns, drain_ns;
