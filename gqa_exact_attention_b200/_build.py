@@ -1,4 +1,5 @@
-"""In-tree build of libgqa_attn.so and libgqa_serve.so (nvcc, sm_100a only)."""
+"""In-tree build of libgqa_attn.so and libgqa_serve.so (nvcc, sm_100a only), and of the module that
+binds the latter to Python."""
 from __future__ import annotations
 
 import glob
@@ -11,6 +12,8 @@ LIB = os.path.join(HERE, "libgqa_attn.so")
 CSRC = os.path.join(HERE, "csrc")
 SERVE_LIB = os.path.join(HERE, "libgqa_serve.so")
 SERVE_CSRC = os.path.join(HERE, "csrc_serve")
+SERVE_BIND = os.path.join(HERE, "_serve_bind.so")
+SERVE_BIND_SRC = os.path.join(HERE, "bind", "serve_bind.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 NVCC_FLAGS = [
@@ -42,6 +45,10 @@ def serve_stale() -> bool:
     return _older(SERVE_LIB, _sources(SERVE_CSRC) + _headers(SERVE_CSRC) + _headers(CSRC))
 
 
+def bind_stale() -> bool:
+    return _older(SERVE_BIND, [SERVE_BIND_SRC])
+
+
 def _older(lib, deps) -> bool:
     if not os.path.exists(lib):
         return True
@@ -62,6 +69,7 @@ def _compile(lib, folders, files, verbose):
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile each library if any of its sources is newer than it; return the forward's path."""
     build_serve(force, verbose)
+    build_bind(force)
     if not force and not _stale():
         return LIB
     return _compile(LIB, [CSRC], sources(), verbose)
@@ -71,6 +79,27 @@ def build_serve(force: bool = False, verbose: bool = False) -> str:
     if not force and not serve_stale():
         return SERVE_LIB
     return _compile(SERVE_LIB, [SERVE_CSRC, CSRC], _sources(SERVE_CSRC), verbose)
+
+
+def build_bind(force: bool = False) -> str:
+    """The binding module, against this interpreter and torch; it finds libgqa_serve.so beside it."""
+    if not force and not bind_stale():
+        return SERVE_BIND
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    paths = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for p in paths:
+        cmd += ["-isystem", p]
+    cmd += [SERVE_BIND_SRC, "-o", SERVE_BIND, "-L", HERE, "-l:libgqa_serve.so", "-Wl,-rpath,$ORIGIN",
+            "-L", libs, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    subprocess.run(cmd, check=True)
+    return SERVE_BIND
 
 
 if __name__ == "__main__":
