@@ -72,9 +72,9 @@ struct Cfg {
     static_assert(kRegsLoad + NT * kRegsSoftmax + kRegsEpilogue == kWarpgroups * kLaunchRegs,
                   "register split must add up to the launch allocation");
     static constexpr int kTmemCols = (NT * 128 + NT * HD) <= 256 ? 256 : 512;
-    // d = 64 with two tiles: S and O take 384 of 512 columns, so P has columns of its own and
+    // d = 64: S and O leave columns for P (two tiles: 384 of 512; one: 192 of 256), so P has its own and
     // the next block's S is computed while this block's softmax runs
-    static constexpr bool kSepP = (HD == 64 && NT == 2);
+    static constexpr bool kSepP = HD == 64;
     static constexpr int kNumBars = 2 * kSlots + 8 * NT + 4 + (kSepP ? 2 * NT : 0) + 2 * kSegs;
     // warps that read the pieces the scheduler posts: producer, MMA, clearing, softmax, epilogue
     static constexpr int kReaders = 3 + 4 * NT + (kEpilogueWG ? 4 : 0);
