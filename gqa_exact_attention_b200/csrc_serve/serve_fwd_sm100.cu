@@ -396,6 +396,13 @@ __device__ __forceinline__ void store32(const ServeParams& p, size_t at, const u
     }
 }
 
+// Four columns of a row of a partial tile.  The tile's 128 rows lie side by side, so that a warp,
+// whose lanes are rows, writes and reads whole lines.
+template <int HD>
+__device__ __forceinline__ float4* part_at(const ServeParams& p, int tile, int col4, int row) {
+    return reinterpret_cast<float4*>(p.part_o) + ((size_t)tile * (HD / 4) + col4) * 128 + row;
+}
+
 // Writes one tile row from TMEM: O / l and LSE = (m + log2 l) ln 2 to out and lse, or (PART) the
 // same in fp32 and log2 units to the piece's slot.  `has`: the tile had keys in this piece;
 // `valid`: the row's result counts (a tree's padding rows give 0 and -inf).  Arrives on o_empty
@@ -406,8 +413,7 @@ __device__ __forceinline__ void write_row(const ServeParams& p, uint32_t o_addr,
                                           uint32_t o_empty_bar) {
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
     const float lse2 = l > 0.f && valid ? m + __log2f(l) : -INFINITY;
-    const size_t part_row = ((size_t)g.slot * NT + t) * 128 + row;
-    const size_t at = PART ? part_row * HD : out_row<MODE>(p, g.b, g.s, rm) * HD;
+    const size_t at = PART ? 0 : out_row<MODE>(p, g.b, g.s, rm) * HD;
     const bool zero = !has || !valid;
 #pragma unroll
     for (int ch = 0; ch < HD / 32; ++ch) {
@@ -423,12 +429,11 @@ __device__ __forceinline__ void write_row(const ServeParams& p, uint32_t o_addr,
         if (!rm.ok || idle) continue;
         if constexpr (PART) {
             if (zero) continue;  // (the join skips a part whose LSE is -inf)
-            float4* dst = reinterpret_cast<float4*>(p.part_o + at + ch * 32);
             const float* f = reinterpret_cast<const float*>(r);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                __stcg(dst + i, make_float4(f[4 * i] * inv_l, f[4 * i + 1] * inv_l, f[4 * i + 2] * inv_l,
-                                            f[4 * i + 3] * inv_l));
+                __stcg(part_at<HD>(p, g.slot * NT + t, ch * 8 + i, row),
+                       make_float4(f[4 * i] * inv_l, f[4 * i + 1] * inv_l, f[4 * i + 2] * inv_l, f[4 * i + 3] * inv_l));
         } else {
             if (zero) {
 #pragma unroll
@@ -438,7 +443,7 @@ __device__ __forceinline__ void write_row(const ServeParams& p, uint32_t o_addr,
         }
     }
     if (rm.ok) {
-        if constexpr (PART) __stcg(p.part_lse + part_row, lse2);
+        if constexpr (PART) __stcg(p.part_lse + ((size_t)g.slot * NT + t) * 128 + row, lse2);
         else p.lse[lse_row<MODE>(p, g.b, g.s, rm)] = lse2 * kLn2;
     }
 }
@@ -1569,14 +1574,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
 // so that units in many parts are spread over as many blocks.  With L_i = log2 of part i's sum,
 // M = max L_i and w_i = 2^(L_i - M), O = sum w_i O_i / sum w_i and LSE = (M + log2 sum w_i) ln 2,
 // in the order of the keys.  The partials come from L2, and the latency of those reads is what
-// it costs: a warp takes four rows at once (lanes = 4 rows x 8 parts for the L_i, then 4 or 2
-// columns of each row) and all blocks are resident at once.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 2;  // per boundary
-constexpr int kJoinRows = 4, kJoinLanes = 32 / kJoinRows;
+// it costs: a warp joins 32 columns of 32 rows (lane = row), with eight reads in flight per part.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinBlocks = 4;  // per boundary
 template <int HD, int NT, int MODE>
-__global__ void __launch_bounds__(kJoinThreads, 4) serve_join_kernel(const __grid_constant__ ServeParams p) {
-    constexpr int kRows = NT * 128;
+__global__ void __launch_bounds__(kJoinThreads) serve_join_kernel(const __grid_constant__ ServeParams p) {
     const int lane = threadIdx.x & 31;
     const int c = (int)blockIdx.x + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1585,78 +1587,36 @@ __global__ void __launch_bounds__(kJoinThreads, 4) serve_join_kernel(const __gri
     Seq s{};
     s.q0 = u.q0;
     s.lq = u.lq;
+    // of the unit's items (32 rows x 32 columns), this boundary's share
+    constexpr int kCols = HD / 32, kItems = NT * 4 * kCols;
     const int shares = (u.parts - 1) * kJoinBlocks, share = (c - u.cta0 - 1) * kJoinBlocks + (int)blockIdx.y;
-    const int r_end = (int)((long long)kRows * (share + 1) / shares);
-    auto row_of = [&](int i, int r) { return (size_t)(i == 0 ? u.first_slot : 2 * (u.cta0 + i)) * kRows + r; };
-    constexpr int kPer = HD / 32;
-    const int part = lane % kJoinLanes;
-    for (int r0 = (int)((long long)kRows * share / shares) + (threadIdx.x >> 5) * kJoinRows; r0 < r_end;
-         r0 += kJoinThreads / 32 * kJoinRows) {
-        const int rl = r0 + lane / kJoinLanes;  // this lane's row for the L_i
-        const RowMap rm = row_map(p, s.lq, (u.mt * NT + rl / 128) * p.pos_per_tile, u.hg, rl % 128);
-        const bool ok = rl < r_end && rm.ok;
+    const int end = kItems * (share + 1) / shares;
+    auto tile_of = [&](int i, int t) { return (i == 0 ? u.first_slot : 2 * (u.cta0 + i)) * NT + t; };
+    for (int item = kItems * share / shares + (threadIdx.x >> 5); item < end; item += kJoinThreads / 32) {
+        const int ch = item % kCols, t = item / kCols / 4, row = item / kCols % 4 * 32 + lane;
+        const RowMap rm = row_map(p, s.lq, (u.mt * NT + t) * p.pos_per_tile, u.hg, row);
+        if (!rm.ok) continue;
         float M = -INFINITY;
-        if (ok)
-            for (int i = part; i < u.parts; i += kJoinLanes) M = fmaxf(M, __ldcg(p.part_lse + row_of(i, rl)));
+        for (int i = 0; i < u.parts; ++i) M = fmaxf(M, __ldcg(p.part_lse + (size_t)tile_of(i, t) * 128 + row));
+        float sum = 0.f;
+        float acc[32] = {};
+        for (int i = 0; i < u.parts; ++i) {
+            const float li = __ldcg(p.part_lse + (size_t)tile_of(i, t) * 128 + row);
+            if (!(li > -INFINITY)) continue;  // no keys in this part: it was not written
+            const float w = ex2_approx(li - M);
+            sum += w;
+            float4 v[8];
 #pragma unroll
-        for (int o = 1; o < kJoinLanes; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float acc[kJoinRows][kPer] = {}, sum = 0.f;
-        for (int i0 = 0; i0 < u.parts; i0 += kJoinLanes) {
-            const float li = ok && i0 + part < u.parts ? __ldcg(p.part_lse + row_of(i0 + part, rl)) : -INFINITY;
-            const float wl = li > -INFINITY ? ex2_approx(li - M) : 0.f;  // 0: no keys in this part
-            sum += wl;
-            const int n = min(kJoinLanes, u.parts - i0);
-#pragma unroll 2
-            for (int j = 0; j < n; ++j) {
-                float v[kJoinRows][kPer], wi[kJoinRows];
+            for (int e = 0; e < 8; ++e) v[e] = __ldcg(part_at<HD>(p, tile_of(i, t), ch * 8 + e, row));
 #pragma unroll
-                for (int e = 0; e < kJoinRows; ++e) {
-                    wi[e] = __shfl_sync(0xffffffffu, wl, e * kJoinLanes + j);
-                    const float* src = p.part_o + row_of(i0 + j, r0 + e) * HD + lane * kPer;
-#pragma unroll
-                    for (int x = 0; x < kPer; ++x) v[e][x] = 0.f;
-                    if (wi[e] != 0.f) {  // (else its rows were not written)
-                        if constexpr (kPer == 4) {
-                            const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
-                            v[e][0] = t.x, v[e][1] = t.y, v[e][2] = t.z, v[e][3] = t.w;
-                        } else {
-                            const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-                            v[e][0] = t.x, v[e][1] = t.y;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < kJoinRows; ++e)
-#pragma unroll
-                    for (int x = 0; x < kPer; ++x) acc[e][x] += wi[e] * v[e][x];
+            for (int e = 0; e < 8; ++e) {
+                acc[4 * e] += w * v[e].x, acc[4 * e + 1] += w * v[e].y;
+                acc[4 * e + 2] += w * v[e].z, acc[4 * e + 3] += w * v[e].w;
             }
         }
-#pragma unroll
-        for (int o = 1; o < kJoinLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (ok && part == 0)
-            p.lse[lse_row<MODE>(p, u.b, s, rm)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
-        const float inv_l = sum > 0.f ? 1.f / sum : 0.f;
-        const long long at_l = ok ? (long long)out_row<MODE>(p, u.b, s, rm) * HD : -1;
-#pragma unroll
-        for (int e = 0; e < kJoinRows; ++e) {
-            const float inv = __shfl_sync(0xffffffffu, inv_l, e * kJoinLanes);
-            const long long row = __shfl_sync(0xffffffffu, at_l, e * kJoinLanes);
-            if (row < 0) continue;
-            const size_t at = (size_t)row + lane * kPer;
-            if (p.out_bf16 != nullptr) {
-                if constexpr (kPer == 4)
-                    *reinterpret_cast<uint2*>(p.out_bf16 + at) = make_uint2(
-                        pack_bf16x2(acc[e][0] * inv, acc[e][1] * inv), pack_bf16x2(acc[e][2] * inv, acc[e][3] * inv));
-                else
-                    *reinterpret_cast<uint32_t*>(p.out_bf16 + at) = pack_bf16x2(acc[e][0] * inv, acc[e][1] * inv);
-            } else {
-                if constexpr (kPer == 4)
-                    *reinterpret_cast<float4*>(p.out + at) =
-                        make_float4(acc[e][0] * inv, acc[e][1] * inv, acc[e][2] * inv, acc[e][3] * inv);
-                else
-                    *reinterpret_cast<float2*>(p.out + at) = make_float2(acc[e][0] * inv, acc[e][1] * inv);
-            }
-        }
+        store32(p, out_row<MODE>(p, u.b, s, rm) * HD + ch * 32, reinterpret_cast<const uint32_t(&)[32]>(acc),
+                sum > 0.f ? 1.f / sum : 0.f);
+        if (ch == 0) p.lse[lse_row<MODE>(p, u.b, s, rm)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
     }
 }
 
