@@ -98,7 +98,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
     const int rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheState& c = p.c;
-    if constexpr (FORK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next();
     const int n = p.n;
     const int size = set_size(n);
     int* key_ = smem;       // [n] the requests
@@ -123,6 +123,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
             parents.first[i] = 0x7fffffff;
         }
     }
+    wait_before();
     for (int i = tid; i < n; i += kThreads) {
         key_[i] = p.key != nullptr ? p.key[i] : i;
         arg_[i] = p.arg[i];
@@ -333,8 +334,9 @@ __global__ void __launch_bounds__(kCopyThreads) cache_tail_copy_kernel(const __g
                                                                        const __grid_constant__ Pools pools) {
     const CacheState& c = p.c;
     const int i = blockIdx.x;
+    let_next();
+    wait_before();
     const int child = p.key[i], parent = p.arg[i];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is done
     if (p.status[i] != GQA_CACHE_DONE || parent == child) return;
     const int len = clamp_len(__ldcg(c.lens + child), c);
     const int tail = len & ((1 << c.page_shift) - 1);
@@ -411,7 +413,8 @@ __global__ void __launch_bounds__(kMoveThreads) cache_compact_rows_kernel(const 
     __shared__ int from_[kMoveRows], to_[kMoveRows];  // rows of a layer's pool; -1: not moved
     const CacheState& c = p.c;
     const int s = blockIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next();
+    wait_before();
     const CompactSlot r = compact_slot(p, s);
     if (blockIdx.y == 0 && threadIdx.x == 0) p.status[s] = r.status;
     if (r.status != GQA_CACHE_DONE) return;
@@ -459,7 +462,8 @@ __global__ void __launch_bounds__(kMoveThreads) cache_compact_rows_kernel(const 
 __global__ void __launch_bounds__(128) cache_compact_pages_kernel(const __grid_constant__ CompactParams p) {
     const CacheState& c = p.c;
     const int s = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows have moved
+    let_next();
+    wait_before();
     if (s >= c.S || p.status[s] != GQA_CACHE_DONE) return;
     const int len = clamp_len(c.lens[s], c);
     const int nodes = min(max(p.tree_lens != nullptr ? p.tree_lens[s] : p.T, 0), min(p.T, len));
@@ -481,28 +485,12 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
                                              (int)bytes);
         if (e != cudaSuccess) return e;
     }
-    cache_plan_kernel<FORK><<<kClusterCtas, kThreads, bytes, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(cache_plan_kernel<FORK>, dim3(kClusterCtas), kThreads, bytes, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_resize(const PlanParams& p, cudaStream_t stream) { return launch_plan<false>(p, stream); }
-
-// A kernel that may be brought in while the one before it still runs, and waits for it itself.
-template <class... A>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t stream, const A&... args) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 cudaError_t launch_fork(const PlanParams& p, const Pools& pools, int sms, cudaStream_t stream) {
     cudaError_t e = launch_plan<true>(p, stream);
@@ -513,7 +501,7 @@ cudaError_t launch_fork(const PlanParams& p, const Pools& pools, int sms, cudaSt
     long long each = ((long long)sms * 16 + p.n - 1) / p.n;
     if (each > pieces) each = pieces;
     if (each > 65535) each = 65535;
-    return launch_after(cache_tail_copy_kernel, dim3((unsigned)p.n, (unsigned)each), kCopyThreads, stream, p, pools);
+    return launch_early(cache_tail_copy_kernel, dim3((unsigned)p.n, (unsigned)each), kCopyThreads, 0, stream, p, pools);
 }
 
 cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t stream) {
@@ -522,10 +510,9 @@ cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t stream)
     long long each = ((long long)sms * 7 + p.c.S - 1) / p.c.S;
     const long long most = (items + kMoveThreads - 1) / kMoveThreads;
     if (each > most) each = most;
-    cache_compact_rows_kernel<<<dim3((unsigned)p.c.S, (unsigned)each), kMoveThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(cache_compact_rows_kernel, dim3((unsigned)p.c.S, (unsigned)each), kMoveThreads, 0, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_after(cache_compact_pages_kernel, dim3((unsigned)((p.c.S + 3) / 4)), 128, stream, p);
+    return launch_early(cache_compact_pages_kernel, dim3((unsigned)((p.c.S + 3) / 4)), 128, 0, stream, p);
 }
 
 }  // namespace gqa

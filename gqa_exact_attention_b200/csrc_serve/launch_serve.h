@@ -6,6 +6,32 @@
 
 namespace gqa {
 
+// Every kernel here but those of large prompt batches may be brought in while the one before it in the stream still runs
+// (programmatic dependent launch): its blocks set themselves up, and wait (wait_before) for all
+// that came before to be complete before they touch global memory.  Its own first act is to let
+// the next one in (let_next), which costs nothing: that one's blocks come when all of its own are
+// placed, and take only room that is free.
+#ifdef __CUDACC__
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... A>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const A&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 // ---------------------------------------------------------------- cache pages
 struct CacheState {
     int* table;  // [S, M]

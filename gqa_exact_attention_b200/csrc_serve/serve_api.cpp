@@ -269,11 +269,14 @@ void fill_common(gqa::ServeParams* p, int B, int Hq, int Hk, float scale, long l
 // The ranges schedule: every CTA slot gets an equal share of all key blocks.  Units of at most
 // kWholeBlocks blocks are not split: a CTA that walks one alone is done before the partials of
 // several would be written and joined, and needs no scratch.
-gqa_status run_ranges(gqa::ServeParams* p, int dev, int sms, int d, int nt, long long most_keys, cudaStream_t stream) {
+gqa_status run_ranges(gqa::ServeParams* p, int dev, int sms, int d, int nt, long long most_units, long long most_keys,
+                      cudaStream_t stream) {
     constexpr int kWholeBlocks = 4;
-    const int grid = sms * gqa::serve_ctas_per_sm(nt);
+    int grid = sms * gqa::serve_ctas_per_sm(nt);
     p->whole = most_keys <= kWholeBlocks * gqa::kServeBlockN ? 1 : 0;
     p->min_blocks = p->whole ? 1 : 2;
+    const long long steps = most_units * (p->whole ? 1 : ceil_div(most_keys, gqa::kServeBlockN));
+    if (steps < grid) grid = (int)(steps > 1 ? steps : 1);
     const bool prefix = p->B > gqa::kServeOwnPrefix;
     if (p->whole && !prefix) return launched(gqa::launch_serve(*p, d, nt, grid, stream));
     const size_t rows = (size_t)2 * grid * nt * gqa::kServeBlockM;
@@ -379,7 +382,7 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (tiles >= 2 && units >= 3ll * info.sms) return run_list(&p, dev, info.sms, d, s);
     p.kv_shared = (tiles > 1 || !p.pack) ? 1 : 0;
-    return run_ranges(&p, dev, info.sms, d, 1, total_k, s);
+    return run_ranges(&p, dev, info.sms, d, 1, (ceil_div(total_q, p.pos_per_tile) + B) * p.n_hg, total_k, s);
 }
 
 gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -444,7 +447,8 @@ gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_c
             return GQA_ERR_CUDA;
     }
     p.kv_shared = (tiles > nt || !p.pack) ? 1 : 0;
-    return run_ranges(&p, dev, info.sms, d, nt, p.cap, static_cast<cudaStream_t>(stream));
+    return run_ranges(&p, dev, info.sms, d, nt, ceil_div(tiles, nt) * B * p.n_hg, p.cap,
+                      static_cast<cudaStream_t>(stream));
 }
 
 gqa_status gqa_cache_resize(int* block_table, int* cache_seqlens, int* page_refs, int S,
