@@ -2,7 +2,7 @@
 //
 // Taking pages is a prefix problem: request i, which needs a_i pages, gets those free pages
 // (page_refs = 0) whose rank among the free ones, in order of their numbers, lies in
-// [a_0 + .. + a_{i-1}, a_0 + .. + a_i).  One cluster of 8 thread blocks does a whole call: it
+// [a_0 + .. + a_{i-1}, a_0 + .. + a_i).  One cluster of thread blocks does a whole call: it
 // validates the requests, gives up and shares pages, counts the free ones per warp, and each
 // warp then writes the ranks of its own pages into the table.  The steps are separated by
 // cluster barriers (a fraction of a microsecond) instead of launches, and the state stays in
@@ -19,7 +19,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kClusterCtas = 8;
+constexpr int kMostCtas = 16;  // of a cluster (8 where 16 cannot be had)
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kEmpty = -1;
@@ -89,13 +89,12 @@ constexpr int kMost = 0x7fffffff;
 __device__ __forceinline__ int saturate(long long x) { return x > kMost ? kMost : (int)x; }
 
 template <bool FORK>
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
-    cache_plan_kernel(const __grid_constant__ PlanParams p) {
+__global__ void __launch_bounds__(kThreads) cache_plan_kernel(const __grid_constant__ PlanParams p) {
     extern __shared__ int smem[];
     __shared__ long long warp_sums[kWarps];
     __shared__ int cta_free;
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank();
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheState& c = p.c;
     let_next();
@@ -182,13 +181,17 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         carry += total;
     }
     const int needed = saturate(carry);
-    cluster.sync();  // every block has read the state
+    auto sync = [&] {
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+    };
+    sync();  // every block has read the state
 
     // ---- 2. pages given up, and with FORK the shared ones named; 256 entries per warp and turn
     constexpr int kChunk = 256;
     const int chunks = (c.M + kChunk - 1) / kChunk;
     const long long items = (long long)n * chunks;
-    for (long long w = (long long)rank * kWarps + warp; w < items; w += kClusterCtas * kWarps) {
+    for (long long w = (long long)rank * kWarps + warp; w < items; w += ctas * kWarps) {
         const int i = (int)(w % n), j0 = (int)(w / n) * kChunk;
         if (!acts(i)) continue;
         const int lo = FORK ? 0 : first[i];
@@ -216,7 +219,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
     // time so that the loads overlap; bit e of a lane's mask is page 32 e + lane
     constexpr int kFew = 32;
     int free_before = 0, free_all = 0;
-    const int per_warp = ((c.P + kClusterCtas * kWarps - 1) / (kClusterCtas * kWarps) + 31) / 32 * 32;
+    const int per_warp = ((c.P + ctas * kWarps - 1) / (ctas * kWarps) + 31) / 32 * 32;
     const long long p0 = (long long)(rank * kWarps + warp) * per_warp;
     const int p_lo = p0 < c.P ? (int)p0 : c.P;
     const int p_hi = p0 + per_warp < c.P ? (int)(p0 + per_warp) : c.P;
@@ -233,7 +236,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         return m;
     };
     if (needed > 0) {
-        cluster.sync();  // the counts are final
+        sync();  // the counts are final
         int mine = 0;
         unsigned first_mask = 0;  // of the warp's first pages: most pools have no more
         for (int at = p_lo; at < p_hi; at += kFew * 32) {
@@ -247,9 +250,9 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
         // (lane 31 of each warp holds the sum up to and with its warp)
         free_before = __shfl_sync(0xffffffffu, incl, 31) - mine;
         if (tid == 0) cta_free = (int)total;
-        cluster.sync();
+        sync();
         // (each of the first lanes reads one block's count)
-        int x = lane < kClusterCtas ? *cluster.map_shared_rank(&cta_free, lane) : 0;
+        int x = lane < ctas ? *cluster.map_shared_rank(&cta_free, lane) : 0;
         free_all = __reduce_add_sync(0xffffffffu, x);
         free_before += __reduce_add_sync(0xffffffffu, lane < rank ? x : 0);
 
@@ -295,7 +298,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
     }
 
     // ---- 5. lengths and outcomes
-    for (int i = rank * kThreads + tid; i < n; i += kClusterCtas * kThreads) {
+    for (int i = rank * kThreads + tid; i < n; i += ctas * kThreads) {
         int st = state[i];
         if (st == kTake) st = upto[i] <= free_all ? GQA_CACHE_DONE : GQA_CACHE_NO_PAGES;
         if constexpr (FORK) {
@@ -309,8 +312,8 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
     if constexpr (FORK) {
         // a child without a page for its last rows gives the shared ones back
         if (needed > free_all) {
-            cluster.sync();  // no warp looks for free pages any more
-            for (int i = rank * kWarps + warp; i < n; i += kClusterCtas * kWarps) {
+            sync();  // no warp looks for free pages any more
+            for (int i = rank * kWarps + warp; i < n; i += ctas * kWarps) {
                 if (state[i] != kTake || upto[i] <= free_all) continue;
                 int* row = row_of(c, key_[i]);
                 for (int j = lane; j < first[i]; j += 32) {
@@ -320,7 +323,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kThreads)
             }
         }
     }
-    if (needed > 0) cluster.sync();  // a block's count is read by the others until here
+    if (needed > 0) sync();  // a block's count is read by the others until here
 }
 
 // The last rows of each fork: [0, len % page) of the parent's last page to the child's, in every
@@ -477,15 +480,56 @@ __global__ void __launch_bounds__(128) cache_compact_pages_kernel(const __grid_c
     if (lane == 0) c.lens[s] = end;
 }
 
+// Blocks of the cluster: enough that a block looks through few thousand pages and a warp gives up
+// or shares few hundred entries (a pool of 131 thousand pages, 256 slots of 2048 entries: 22 us
+// with 8 blocks), and one for a small cache, whose steps then need no cluster barrier.
+int plan_ctas(const PlanParams& p) {
+    const long long pages = ((long long)p.c.P + 8191) / 8192, entries = (long long)p.n * ((p.c.M + 255) / 256) / 64;
+    int ctas = 1;
+    while (ctas < kMostCtas && ctas < (pages > entries ? pages : entries)) ctas *= 2;
+    return ctas;
+}
+
 template <bool FORK>
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
     const size_t bytes = sizeof(int) * (6 * (size_t)p.n + (FORK ? 4 : 2) * (size_t)set_size(p.n));
-    if (bytes > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(cache_plan_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)bytes);
+    // per device, set once for the most that a call may need; setting it again is harmless
+    static int most_ctas[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {kMostCtas, 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kMostCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    int most = dev >= 0 && dev < 64 ? most_ctas[dev] : 0;
+    if (most == 0) {
+        const size_t largest = sizeof(int) * (6 * (size_t)GQA_CACHE_MAX_REQUESTS +
+                                              (FORK ? 4 : 2) * (size_t)set_size(GQA_CACHE_MAX_REQUESTS));
+        e = cudaFuncSetAttribute(cache_plan_kernel<FORK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)largest);
         if (e != cudaSuccess) return e;
+        most = 8;  // what every device can place
+        int clusters = 0;
+        cfg.dynamicSmemBytes = largest;
+        if (cudaFuncSetAttribute(cache_plan_kernel<FORK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&clusters, cache_plan_kernel<FORK>, &cfg) == cudaSuccess && clusters > 0)
+            most = kMostCtas;
+        cudaGetLastError();
+        cfg.dynamicSmemBytes = bytes;
+        if (dev >= 0 && dev < 64) most_ctas[dev] = most;
     }
-    return launch_early(cache_plan_kernel<FORK>, dim3(kClusterCtas), kThreads, bytes, stream, p);
+    const int ctas = plan_ctas(p) < most ? plan_ctas(p) : most;
+    cfg.gridDim = dim3((unsigned)ctas);
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    return cudaLaunchKernelEx(&cfg, cache_plan_kernel<FORK>, p);
 }
 
 }  // namespace
