@@ -75,7 +75,7 @@ struct Cfg {
     // d = 64: S and O leave columns for P (two tiles: 384 of 512; one: 192 of 256), so P has its own and
     // the next block's S is computed while this block's softmax runs
     static constexpr bool kSepP = HD == 64;
-    static constexpr int kNumBars = 2 * kSlots + 8 * NT + 4 + (kSepP ? 2 * NT : 0) + 2 * kSegs;
+    static constexpr int kNumBars = 2 * kSlots + 9 * NT + 4 + (kSepP ? 2 * NT : 0) + 2 * kSegs;
     // warps that read the pieces the scheduler posts: producer, MMA, clearing, softmax, epilogue
     static constexpr int kReaders = 3 + 4 * NT + (kEpilogueWG ? 4 : 0);
     static constexpr int kStatsBytes = kEpilogueWG ? 2 * NT * 2 * 128 * 4 : 0;  // (m, l), 2 buffers
@@ -606,9 +606,13 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
     // cleared (warp 2 -> MMA).  Warp 2 does not follow the ring by itself: it would miss phases.
     const uint32_t v_dirty = bar0 + 8u * (2 * C::kSlots + 8 * NT + 3);
     const uint32_t v_clean = bar0 + 8u * (2 * C::kSlots + 8 * NT + 2);
+    // the first half of P_t (64 keys) is there: its P V runs while the softmax does the second
+    // (not with separate P: there S runs meanwhile, and the hand-off cost 2 % at d = 64; at
+    // d = 128 it gains 1-4 %)
+    [[maybe_unused]] auto p_half = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 8 * NT + 4 + t); };
     // separate P (kSepP): S_t read into registers (softmax -> MMA), P_t.V done (MMA -> softmax)
-    [[maybe_unused]] auto s_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 8 * NT + 4 + t); };
-    [[maybe_unused]] auto p_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 8 * NT + 4 + NT + t); };
+    [[maybe_unused]] auto s_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 9 * NT + 4 + t); };
+    [[maybe_unused]] auto p_free = [&](int t) { return bar0 + 8u * (2 * C::kSlots + 9 * NT + 4 + NT + t); };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -623,6 +627,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
             mbar_init(q_full(t), 1);
             mbar_init(q_empty(t), 1);
             mbar_init(s_full(t), 1);
+            mbar_init(p_half(t), 128);
             mbar_init(p_full(t), 128);
             mbar_init(o_full(t), 1);
             mbar_init(o_empty(t), 128);
@@ -821,20 +826,19 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 }
                 return __ballot_sync(0xffffffffu, ready) != 0u;  // only the issuing lane probed
             };
-            // O_t += P_t V over the block's 128 keys
-            auto issue_pv = [&](int t, int slot, bool accumulate, uint32_t probe_bar,
-                                uint32_t probe_par) {
-                const uint64_t b0 = sdesc_add(v_desc0, slot * C::kTileBytes);
+            // O_t += P_t V over half h of the block's keys; before the last MMA, probe as above
+            auto issue_pv = [&](int t, int slot, int h, bool accumulate, uint32_t probe_bar, uint32_t probe_par) {
+                constexpr int kSteps = C::kPvSteps / 2;
+                const uint64_t b0 = sdesc_add(v_desc0, slot * C::kTileBytes + h * kSteps * C::kPvStepBytes);
                 const uint32_t d = tmem + C::o_col(t);
-                const uint32_t a = tmem + C::p_col(t);
+                const uint32_t a = tmem + C::p_col(t) + h * kSteps * 8;
                 bool ready = false;
                 if (elect_one()) {
-                    // 8 TMEM columns of P per MMA (16 bf16 or 32 e4m3 keys)
+                    // 8 TMEM columns of P (16 keys) per MMA
 #pragma unroll
-                    for (int kk = 0; kk < C::kPvSteps; ++kk) {
-                        if (kk == C::kPvSteps - 1 && probe_bar != 0u) ready = mbar_test_wait(probe_bar, probe_par);
-                        C::mma_pv(d, a + kk * 8, sdesc_add(b0, kk * C::kPvStepBytes),
-                                  (accumulate || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < kSteps; ++kk) {
+                        if (kk == kSteps - 1 && probe_bar != 0u) ready = mbar_test_wait(probe_bar, probe_par);
+                        C::mma_pv(d, a + kk * 8, sdesc_add(b0, kk * C::kPvStepBytes), (accumulate || kk > 0) ? 1u : 0u);
                     }
                 }
                 return __ballot_sync(0xffffffffu, ready) != 0u;  // only the issuing lane probed
@@ -915,7 +919,8 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                             if (!ok) break;
                         }
                         tc_fence_after();
-                        issue_pv(t, slot_v, it > 0, 0u, 0u);
+                        issue_pv(t, slot_v, 0, it > 0, 0u, 0u);
+                        issue_pv(t, slot_v, 1, true, 0u, 0u);
                         commit(p_free(t));
                         if (it + 1 == g.n[t]) {
                             commit(o_full(t));
@@ -1004,21 +1009,24 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         if (it >= g.n[t] || !ok) continue;
-                        if (!p_ready) ok = wait(p_full(t), pn[t] & 1u);
+                        if (!p_ready) ok = wait(p_half(t), pn[t] & 1u);
                         if (!ok) break;
-                        ++pn[t];
                         if (it == 0 && on[t] > 0) {
                             // the previous unit's epilogue must have read O_t out
                             ok = wait(o_empty(t), (on[t] - 1) & 1u);
                             if (!ok) break;
                         }
                         tc_fence_after();
+                        if (!issue_pv(t, slot_v, 0, it > 0, p_full(t), pn[t] & 1u)) ok = wait(p_full(t), pn[t] & 1u);
+                        if (!ok) break;
+                        ++pn[t];
+                        tc_fence_after();
                         const bool more = it + 1 < g.n[t];
                         // probe what comes next: this tile's next K, else the next tile's P
                         const bool has_next_tile = (t + 1 < NT) && (it < g.n[t + 1 < NT ? t + 1 : t]);
-                        const uint32_t pbar_next = has_next_tile ? p_full(t + 1 < NT ? t + 1 : t) : 0u;
+                        const uint32_t pbar_next = has_next_tile ? p_half(t + 1 < NT ? t + 1 : t) : 0u;
                         const uint32_t ppar_next = has_next_tile ? (pn[t + 1 < NT ? t + 1 : t] & 1u) : 0u;
-                        bool probed = issue_pv(t, slot_v, it > 0,
+                        bool probed = issue_pv(t, slot_v, 1, true,
                                                more && !k_ready ? kbar : pbar_next,
                                                more && !k_ready ? kpar : ppar_next);
                         if (more) {
@@ -1191,6 +1199,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                             if (!ok) break;
                         }
                     }
+                    if constexpr (!C::kSepP) mbar_arrive(p_half(t));
                     mbar_arrive(p_full(t));
                 }
                 if (!ok) break;
@@ -1397,6 +1406,11 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                             r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
                         tmem_st32(o_addr + ch * 32, r);
                     }
+                }
+                if constexpr (!C::kSepP) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(p_half(t));
                 }
                 // second half: keys 64..127
                 if (masked) exp_range(std::true_type{}, 2, 4);
