@@ -343,7 +343,7 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
         !stride_ok(&v_row_stride, (long long)Hk * d))
         return GQA_ERR_SHAPE;
     // kernel row indices are 32-bit
-    if ((long long)total_q * Hq >= (1ll << 31) || (long long)total_k * Hk >= (1ll << 31)) return GQA_ERR_SHAPE;
+    if (((long long)total_q + B) * Hq >= (1ll << 31) || (long long)total_k * Hk >= (1ll << 31)) return GQA_ERR_SHAPE;
     if (!cu_seqlens_q || !cu_seqlens_k) return GQA_ERR_NULL;
     if (total_q > 0 && (!q || !out || !lse)) return GQA_ERR_NULL;
     if (total_k > 0 && (!k || !v)) return GQA_ERR_NULL;

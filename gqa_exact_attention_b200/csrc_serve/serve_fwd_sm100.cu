@@ -135,6 +135,11 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// A small input (a bound, a length, a table entry, a mask word), from L2: the kernel may have
+// started before the one that writes it ended, so no read-only path.
+template <class T>
+__device__ __forceinline__ T fresh(const T* p) { return __ldcg(p); }
+
 // ---------------------------------------------------------------- sequences, units, segments
 
 struct Seq {
@@ -146,16 +151,16 @@ template <int MODE>
 __device__ __forceinline__ Seq seq_of(const ServeParams& p, int b) {
     Seq s;
     if constexpr (MODE == kVarlenRanges || MODE == kVarlenList) {
-        s.q0 = min(max(__ldg(p.cu_q + b), 0), p.total_q);
-        s.lq = min(max(__ldg(p.cu_q + b + 1), s.q0), p.total_q) - s.q0;
-        s.k0 = min(max(__ldg(p.cu_k + b), 0), p.total_k);
-        s.sk = min(max(__ldg(p.cu_k + b + 1), s.k0), p.total_k) - s.k0;
+        s.q0 = min(max(fresh(p.cu_q + b), 0), p.total_q);
+        s.lq = min(max(fresh(p.cu_q + b + 1), s.q0), p.total_q) - s.q0;
+        s.k0 = min(max(fresh(p.cu_k + b), 0), p.total_k);
+        s.sk = min(max(fresh(p.cu_k + b + 1), s.k0), p.total_k) - s.k0;
         s.nodes = 0;
     } else {
         s.q0 = s.k0 = 0;
         s.lq = p.T;
-        s.sk = min(max(__ldg(p.seqlens + b), 0), p.cap);
-        s.nodes = min(max(p.tree_lens != nullptr ? __ldg(p.tree_lens + b) : p.T, 0), min(p.T, s.sk));
+        s.sk = min(max(fresh(p.seqlens + b), 0), p.cap);
+        s.nodes = min(max(p.tree_lens != nullptr ? fresh(p.tree_lens + b) : p.T, 0), min(p.T, s.sk));
     }
     return s;
 }
@@ -255,7 +260,7 @@ __device__ __forceinline__ Walk walk_begin(const ServeParams& p, const long long
     Walk w{};
     if constexpr (MODE == kVarlenList) {
         w.ctas = (int)gridDim.x;
-        w.all = (long long)__ldg(p.list_len) * p.n_hg;
+        w.all = (long long)fresh(p.list_len) * p.n_hg;
         w.x = blockIdx.x;
         w.x_end = w.all;
     } else {
@@ -280,7 +285,7 @@ __device__ __forceinline__ bool next_seg(Walk& w, Seg<NT>& g, const ServeParams&
         const int at = (r & 1) && (long long)(r + 1) * w.ctas <= w.all ? r * w.ctas + w.ctas - 1 - k : u;
         uint32_t pair, hg;
         fastdivmod((uint32_t)at, p.div_hg, pair, hg);
-        const int2 e = __ldg(p.list + pair);
+        const int2 e = fresh(p.list + pair);
         g.b = e.x;
         g.hg = (int)hg;
         mt = e.y;
@@ -414,7 +419,7 @@ __device__ __forceinline__ void write_row(const ServeParams& p, uint32_t o_addr,
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
     const float lse2 = l > 0.f && valid ? m + __log2f(l) : -INFINITY;
     const size_t at = PART ? 0 : out_row<MODE>(p, g.b, g.s, rm) * HD;
-    const bool zero = !has || !valid;
+    const bool zero = !has || !valid || l == 0.f;  // (no key: 0, whatever V holds)
 #pragma unroll
     for (int ch = 0; ch < HD / 32; ++ch) {
         uint32_t r[32];
@@ -466,7 +471,7 @@ struct PageCache {
     int w0 = -1, w1 = -1;
 };
 __device__ __forceinline__ int table_entry(const ServeParams& p, int b, int i) {
-    return (i < p.table_stride) ? __ldg(p.block_table + (size_t)b * p.table_stride + i) : -1;
+    return (i < p.table_stride) ? fresh(p.block_table + (size_t)b * p.table_stride + i) : -1;
 }
 __device__ __forceinline__ int page_of(PageCache& pc, const ServeParams& p, int b, int page_i,
                                        int lane) {
@@ -519,7 +524,7 @@ __device__ __forceinline__ uint32_t tree_word(const int* row, int i, int nodes) 
     if (i < 0) return 0xffffffffu;
     const int left = nodes - i * 32;
     if (left <= 0) return 0u;
-    const uint32_t w = row != nullptr ? (uint32_t)__ldg(row + i) : 0xffffffffu;
+    const uint32_t w = row != nullptr ? (uint32_t)fresh(row + i) : 0xffffffffu;
     return left >= 32 ? w : w & ((1u << left) - 1u);
 }
 
@@ -1488,7 +1493,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 }
                 const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
                 const float lse_v = (l > 0.f && valid) ? (m + __log2f(l)) * kLn2 : -INFINITY;
-                const bool zero = !has || idle || !valid;
+                const bool zero = !has || idle || !valid || l == 0.f;  // (no key: 0, whatever V holds)
                 // A stage row is 128 bytes: 32 fp32 or 64 bf16 columns.  A full tile leaves by a TMA
                 // store; in a tile that the sequence's end cuts, the rows behind it belong to the
                 // next sequence, and its own are stored one by one.  (A tree's tiles end where the
@@ -1662,8 +1667,8 @@ __global__ void __launch_bounds__(1024) serve_list_kernel(const __grid_constant_
     if (tid == 0) most = 1;
     __syncthreads();
     auto bounds = [](const int* cu, int b, int total, int* lo, int* n) {
-        *lo = min(max(__ldg(cu + b), 0), total);
-        *n = min(max(__ldg(cu + b + 1), *lo), total) - *lo;
+        *lo = min(max(fresh(cu + b), 0), total);
+        *n = min(max(fresh(cu + b + 1), *lo), total) - *lo;
     };
     for (int b = tid; b < p.B; b += 1024) {
         int k0, sk;

@@ -52,7 +52,7 @@ def varlen(q=16, qs=0, k=16, ks=0, v=16, vs=0, cq=16, ck=16, out=16, dt=0, lse=1
     (dict(B=0), 2), (dict(tq=-1), 2), (dict(tk=-1), 2), (dict(Hq=0), 2), (dict(Hk=0), 2), (dict(dt=2), 2),
     (dict(scale=float("nan")), 2),
     (dict(qs=255), 2), (dict(qs=260), 2), (dict(ks=120), 2), (dict(vs=64), 2), (dict(qs=-256), 2), (dict(ks=1 << 40), 2),
-    (dict(tq=1 << 30), 2), (dict(tk=1 << 30), 2),
+    (dict(tq=1 << 30), 2), (dict(B=1 << 30), 2), (dict(tk=1 << 30), 2),
     (dict(Hq=6, Hk=4), 3), (dict(d=96), 4), (dict(q=24), 5), (dict(out=8), 5), (dict(cq=18), 5), (dict(ck=17), 5),
 ])
 def test_varlen_refusals(kw, code):
