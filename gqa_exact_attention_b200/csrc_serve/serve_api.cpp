@@ -367,9 +367,7 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
     p.lse = lse;
     const int g = p.g, M = gqa::kServeBlockM;
     const int box_h = p.pack ? g : 1, box_s = p.pos_per_tile;
-    if (!encode(&p.tm_q, q, 1, total_q, Hq, d, q_row_stride * 2, box_h, box_s) ||
-        !encode(&p.tm_o, out, 1, total_q, Hq, d, (long long)Hq * d * (p.out ? 4 : 2), box_h, box_s, p.out != nullptr))
-        return GQA_ERR_CUDA;
+    if (!encode(&p.tm_q, q, 1, total_q, Hq, d, q_row_stride * 2, box_h, box_s)) return GQA_ERR_CUDA;
     // (without keys nothing is loaded: any mapped address serves)
     const bool keys = total_k > 0;
     if (!encode(&p.tm_k, keys ? k : q, 1, keys ? total_k : 1, keys ? Hk : 1, d, keys ? k_row_stride * 2 : 256, 1, M) ||
@@ -380,7 +378,11 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
     const long long tiles = ceil_div(queries, p.pos_per_tile);
     const long long units = ceil_div(total_q, 2 * p.pos_per_tile) * p.n_hg;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (tiles >= 2 && units >= 3ll * info.sms) return run_list(&p, dev, info.sms, d, s);
+    if (tiles >= 2 && units >= 3ll * info.sms) {
+        if (!encode(&p.tm_o, out, 1, total_q, Hq, d, (long long)Hq * d * (p.out ? 4 : 2), box_h, box_s, p.out != nullptr))
+            return GQA_ERR_CUDA;
+        return run_list(&p, dev, info.sms, d, s);
+    }
     p.kv_shared = (tiles > 1 || !p.pack) ? 1 : 0;
     return run_ranges(&p, dev, info.sms, d, 1, (ceil_div(total_q, p.pos_per_tile) + B) * p.n_hg, total_k, s);
 }
@@ -427,7 +429,8 @@ gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const void* v_c
     const int nt = tiles >= 2 ? 2 : 1, M = gqa::kServeBlockM;
     const int box_h = p.pack ? p.g : 1, box_s = p.pos_per_tile;
     if (!encode(&p.tm_q, q, B, T, Hq, d, 2ll * Hq * d, box_h, box_s) ||
-        !encode(&p.tm_o, out, B, T, Hq, d, (long long)Hq * d * (p.out ? 4 : 2), box_h, box_s, p.out != nullptr))
+        (nt == 2 &&
+         !encode(&p.tm_o, out, B, T, Hq, d, (long long)Hq * d * (p.out ? 4 : 2), box_h, box_s, p.out != nullptr)))
         return GQA_ERR_CUDA;
     const long long kv_row = 2ll * Hk * d;
     if (block_table == nullptr) {

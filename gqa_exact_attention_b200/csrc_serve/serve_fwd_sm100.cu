@@ -135,10 +135,10 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// A small input (a bound, a length, a table entry, a mask word), from L2: the kernel may have
-// started before the one that writes it ended, so no read-only path.
+// A small input (a bound, a length, a table entry, a mask word).  An ordinary load: the kernel may
+// have started before the one that writes it ended, so the read-only path (__ldg) is not for it.
 template <class T>
-__device__ __forceinline__ T fresh(const T* p) { return __ldcg(p); }
+__device__ __forceinline__ T fresh(const T* p) { return *p; }
 
 // ---------------------------------------------------------------- sequences, units, segments
 

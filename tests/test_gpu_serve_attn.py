@@ -387,3 +387,82 @@ def test_captured_graphs(scale):
     for call, _, _, got in pairs:
         for a, b in zip(got, call()):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- nothing else is written
+
+class Canary:
+    """A tensor inside a buffer of a pattern that no result has."""
+
+    def __init__(self, shape, dtype, pad=4096):
+        self.n, self.pad = int(np.prod(shape)), pad
+        self.buf = torch.full((self.n + 2 * pad,), -123.0, dtype=dtype, device="cuda")
+        self.t = self.buf[pad:pad + self.n].view(shape)
+
+    def untouched(self):
+        return bool((self.buf[:self.pad] == -123.0).all() and (self.buf[self.pad + self.n:] == -123.0).all())
+
+    def written(self):
+        return not bool((self.t == -123.0).any())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,Hq,Hk,d", [([33, 1, 0, 127], 6, 2, 64), ([700, 900, 1, 640, 513], 32, 8, 128),
+                                          ([300, 5000], 8, 2, 64), ([900, 700, 650], 64, 8, 64)])
+def test_varlen_writes_its_outputs_and_nothing_else(lens, Hq, Hk, d, dtype):
+    rng = np.random.default_rng(50)
+    q, k, v = (randn(rng, sum(lens), H, d).cuda() for H in (Hq, Hk, Hk))
+    out, lse = Canary((sum(lens), Hq, d), dtype), Canary((Hq, sum(lens)), torch.float32)
+    G.gqa_attn_fwd_varlen(q, k, v, cu(lens), out=out.t, lse=lse.t, causal=True)
+    torch.cuda.synchronize()
+    assert out.untouched() and lse.untouched() and out.written() and lse.written()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,Hq,Hk,d", [(1, 8, 2, 64), (31, 8, 2, 128), (45, 8, 2, 128), (100, 6, 2, 64)])
+def test_tree_writes_its_outputs_and_nothing_else(T, Hq, Hk, d, dtype):
+    rng = np.random.default_rng(51)
+    B, cap = 3, 1500
+    q, k, v = randn(rng, B, T, Hq, d).cuda(), randn(rng, B, cap, Hk, d).cuda(), randn(rng, B, cap, Hk, d).cuda()
+    sl = torch.tensor([1500, 7, 0], dtype=torch.int32, device="cuda")
+    out, lse = Canary((B, T, Hq, d), dtype), Canary((B, Hq, T), torch.float32)
+    G.gqa_attn_fwd_tree(q, k, v, bits(tree(rng, T)), sl, out=out.t, lse=lse.t)
+    torch.cuda.synchronize()
+    assert out.untouched() and lse.untouched() and out.written() and lse.written()
+
+
+@pytest.mark.parametrize("cap", [600, 20000])
+def test_one_sequence_shared_by_all_ctas(cap):
+    """A unit in many parts: one kv head, one long sequence."""
+    run_tree(np.random.default_rng(52), [cap], 5, 4, 1, 128, 64)
+    run_varlen(np.random.default_rng(53), [3], [cap], 4, 1, 64, True, bf16=True)
+
+
+def test_a_given_stream():
+    rng = np.random.default_rng(55)
+    lens = [64, 300]
+    a, b, c = (randn(rng, sum(lens), H, 64).cuda() for H in (4, 2, 2))
+    x = G.gqa_attn_fwd_varlen(a, b, c, cu(lens), causal=True)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    y = G.gqa_attn_fwd_varlen(a, b, c, cu(lens), causal=True, stream=s)
+    s.synchronize()
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    with pytest.raises(ValueError):
+        G.gqa_attn_fwd_varlen(a, b, c, cu(lens), stream=7)
+
+
+def test_random_shapes_of_the_whole_range():
+    """Shapes drawn over the range, against the 64-bit implementation on a sample of heads."""
+    rng = np.random.default_rng(56)
+    for _ in range(12):
+        Hk, g, d = int(rng.choice([1, 2, 4])), int(rng.choice([1, 2, 3, 5, 8])), int(rng.choice([64, 128]))
+        B = int(rng.integers(1, 7))
+        lq = [int(x) for x in rng.integers(0, int(rng.choice([5, 80, 600])), B)]
+        lk = [a + int(x) for a, x in zip(lq, rng.integers(0, int(rng.choice([1, 900])), B))]
+        run_varlen(rng, lq, lk, Hk * g, Hk, d, bool(rng.integers(2)), bool(rng.integers(2)),
+                   start=int(rng.integers(0, 3)), after=int(rng.integers(0, 200)))
+        T = int(rng.choice([1, 3, 17, 64, 90]))
+        lens = [int(x) for x in rng.integers(0, 1500, B)]
+        run_tree(rng, lens, T, Hk * g, Hk, d, int(rng.choice([0, 16, 32, 128, 512])),
+                 n=[int(x) for x in rng.integers(0, T + 2, B)] if rng.integers(2) else None, bf16=bool(rng.integers(2)))

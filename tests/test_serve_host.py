@@ -150,3 +150,18 @@ def test_the_binding_refuses_host_tensors_and_wrong_types():
         G.gqa_cache_fork(_h(8, 16, 2, 64), _h(8, 16, 2, 64), _i(4, 4), _i(4), _i(8), _i(1), _i(1))
     with pytest.raises(ValueError):
         G.gqa_cache_compact(_h(8, 16, 2, 64), _h(8, 16, 2, 64), _i(4, 4), _i(4), _i(8), _i(4, 2), _i(4))
+
+
+def test_ranges_cut_the_steps_without_a_gap():
+    """The arithmetic of the ranges schedule: CTA c takes steps [floor(all c / n), floor(all (c + 1)
+    / n)), and the CTA of step x is ((x + 1) n - 1) // all; no range is empty when n <= all."""
+    import random
+    r = random.Random(1)
+    for _ in range(300):
+        n = r.randint(1, 300)
+        steps = r.choice([n, n + 1, r.randint(n, 10 * n), r.randint(n, 10 ** 9)])
+        start = [steps * c // n for c in range(n + 1)]
+        assert start[0] == 0 and start[n] == steps and all(a < b for a, b in zip(start, start[1:]))
+        for x in [0, steps - 1] + [r.randrange(steps) for _ in range(30)] + [s for s in start[:-1][:40]]:
+            c = ((x + 1) * n - 1) // steps
+            assert start[c] <= x < start[c + 1]
