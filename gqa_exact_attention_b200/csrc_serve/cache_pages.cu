@@ -6,8 +6,10 @@
 // validates the requests, gives up and shares pages, counts the free ones per warp, and each
 // warp then writes the ranks of its own pages into the table.  The steps are separated by
 // cluster barriers (a fraction of a microsecond) instead of launches, and the state stays in
-// L2, so a call costs about one launch.  Nothing depends on the order in which atomics land:
-// the counts only add up.
+// L2.  Nothing depends on the order in which atomics land: the counts only add up.  What a call
+// costs is latency, the dependent reads of its steps (lengths, table entries, counts): measured on
+// B200, 4 us for 8 slots of a small cache, 21 us for 256 slots over 131 thousand pages, whose bytes
+// alone would take 1 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -20,8 +22,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMostCtas = 16;  // of a cluster (8 where 16 cannot be had)
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;  // at most 32: one warp adds them up
 constexpr int kEmpty = -1;
 
 __device__ __forceinline__ int pages_of(int len, int shift) { return (len >> shift) + ((len & ((1 << shift) - 1)) != 0); }
@@ -74,7 +76,7 @@ __device__ long long block_scan(long long x, long long* warp_sums, long long* to
     }
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
-    long long w = warp_sums[lane];
+    long long w = lane < kWarps ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, w, o);
@@ -284,10 +286,10 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(const __grid_const
                         if (upto[mid] > r) hi = mid;
                         else lo = mid + 1;
                     }
-                    if (upto[lo] <= free_all) {
-                        const int before = lo > 0 ? upto[lo - 1] : 0;
+                    const int entry = first[lo] + (r - (lo > 0 ? upto[lo - 1] : 0));
+                    if (upto[lo] <= free_all && entry < c.M) {
                         const int page = at + e * 32 + lane;
-                        row_of(c, key_[lo])[first[lo] + (r - before)] = page;
+                        row_of(c, key_[lo])[entry] = page;
                         c.refs[page] = 1;
                     }
                 }
@@ -329,7 +331,8 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(const __grid_const
 // The last rows of each fork: [0, len % page) of the parent's last page to the child's, in every
 // layer's K and V.  A block belongs to one fork (blockIdx.x) and takes every gridDim.y-th of its
 // pieces, 16 KB of one page in one layer; what it has to look up, it looks up once.  Bound by the
-// bytes: a parent's rows are read from DRAM once and by its other children from L2.
+// bytes: a parent's rows are read from DRAM once and by its other children from L2.  Measured on
+// B200: 226 MB (240 forks of 16 parents, 8 layers) in 46 us, 4.9 TB/s.
 constexpr int kCopyBytes = 16384;
 constexpr int kCopyThreads = 256;
 
@@ -408,7 +411,8 @@ __device__ CompactSlot compact_slot(const CompactParams& p, int s) {
 // Moves the accepted rows.  A thread owns one 16-byte column of one layer's K or V and walks
 // the accepted nodes in order: node keep[j] >= j goes to place j, so a row is overwritten only
 // after it was read, and eight rows may be read before their eight writes.  The rows' places are
-// looked up by the block together, kMoveRows at a time.
+// looked up by the block together, kMoveRows at a time.  Bound by the latency of those look-ups and
+// two turns of reads: measured on B200, 73 MB (128 slots, trees of 64, 8 layers) in 16 us, 4.5 TB/s.
 constexpr int kMoveThreads = 128;
 constexpr int kMoveBatch = 8;
 constexpr int kMoveRows = 128;
@@ -480,11 +484,13 @@ __global__ void __launch_bounds__(128) cache_compact_pages_kernel(const __grid_c
     if (lane == 0) c.lens[s] = end;
 }
 
-// Blocks of the cluster: enough that a block looks through few thousand pages and a warp gives up
-// or shares few hundred entries (a pool of 131 thousand pages, 256 slots of 2048 entries: 22 us
-// with 8 blocks), and one for a small cache, whose steps then need no cluster barrier.
+// Blocks of the cluster: a block for every 1024 pages of the pool or 8 warp turns of table entries,
+// at most 16; one for a small cache, whose steps then need no cluster barrier.  Measured on B200
+// with the calls around them: 131 thousand pages and 256 slots of 2048 entries, 21 us a call (25 with
+// 8 blocks of twice the threads); 4 thousand pages and 128 slots, a verification step of 34 us
+// (39 with a block for every 8192 pages).
 int plan_ctas(const PlanParams& p) {
-    const long long pages = ((long long)p.c.P + 8191) / 8192, entries = (long long)p.n * ((p.c.M + 255) / 256) / 64;
+    const long long pages = ((long long)p.c.P + 1023) / 1024, entries = (long long)p.n * ((p.c.M + 255) / 256) / 8;
     int ctas = 1;
     while (ctas < kMostCtas && ctas < (pages > entries ? pages : entries)) ctas *= 2;
     return ctas;
