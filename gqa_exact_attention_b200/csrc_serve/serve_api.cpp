@@ -268,7 +268,10 @@ void fill_common(gqa::ServeParams* p, int B, int Hq, int Hk, float scale, long l
 
 // The ranges schedule: every CTA slot gets an equal share of all key blocks.  Units of at most
 // kWholeBlocks blocks are not split: a CTA that walks one alone is done before the partials of
-// several would be written and joined, and needs no scratch.
+// several would be written and joined, and needs no scratch.  Measured on B200 (a tree of 8 nodes,
+// B 1, Hk 8, d 128; whole against split): 256 keys 10.2 and 11.9 us, 512 keys 13.4 and 15.1, 1024
+// keys 20.0 and 17.7, 2048 keys 33.3 and 17.4.  A range holds at least two blocks: 8192 keys take
+// 28.5 us so, 25.0 with four and 28.8 with eight, 2048 keys 17.4, 22.4 and 26.6.
 gqa_status run_ranges(gqa::ServeParams* p, int dev, int sms, int d, int nt, long long most_units, long long most_keys,
                       cudaStream_t stream) {
     constexpr int kWholeBlocks = 4;
@@ -373,12 +376,14 @@ gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, const void
     if (!encode(&p.tm_k, keys ? k : q, 1, keys ? total_k : 1, keys ? Hk : 1, d, keys ? k_row_stride * 2 : 256, 1, M) ||
         !encode(&p.tm_v, keys ? v : q, 1, keys ? total_k : 1, keys ? Hk : 1, d, keys ? v_row_stride * 2 : 256, 1, M))
         return GQA_ERR_CUDA;
-    // Two-tile units from a list when the average sequence fills them and there are a few per SM;
-    // else ranges over one-tile units, which also share a long key axis among CTAs.
+    // Two-tile units from a list when the average sequence fills them and there is one for three in
+    // four SMs; else ranges over one-tile units, which also share a long key axis among CTAs.
+    // Measured on B200 (Hq 32, Hk 8, d 128, causal; list against ranges): 64 units 22.8 and 16.1 us,
+    // 128 units 30.9 and 33.3, 256 units 43 and 52, 1024 units 117 and 173.
     const long long tiles = ceil_div(queries, p.pos_per_tile);
     const long long units = ceil_div(total_q, 2 * p.pos_per_tile) * p.n_hg;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (tiles >= 2 && units >= 3ll * info.sms) {
+    if (tiles >= 2 && 4 * units >= 3ll * info.sms) {
         if (!encode(&p.tm_o, out, 1, total_q, Hq, d, (long long)Hq * d * (p.out ? 4 : 2), box_h, box_s, p.out != nullptr))
             return GQA_ERR_CUDA;
         return run_list(&p, dev, info.sms, d, s);
