@@ -331,8 +331,9 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(const __grid_const
 // The last rows of each fork: [0, len % page) of the parent's last page to the child's, in every
 // layer's K and V.  A block belongs to one fork (blockIdx.x) and takes every gridDim.y-th of its
 // pieces, 16 KB of one page in one layer; what it has to look up, it looks up once.  Bound by the
-// bytes: a parent's rows are read from DRAM once and by its other children from L2.  Measured on
-// B200: 226 MB (240 forks of 16 parents, 8 layers) in 46 us, 4.9 TB/s.
+// bytes written: a parent's rows are read from DRAM once and by its other children from L2.
+// Measured on B200: 226 MB (240 forks of 16 parents, 8 layers) in 40 us, 5.6 TB/s; a memset of as
+// much writes 3.7 TB/s.
 constexpr int kCopyBytes = 16384;
 constexpr int kCopyThreads = 256;
 
@@ -545,10 +546,11 @@ cudaError_t launch_resize(const PlanParams& p, cudaStream_t stream) { return lau
 cudaError_t launch_fork(const PlanParams& p, const Pools& pools, int sms, cudaStream_t stream) {
     cudaError_t e = launch_plan<true>(p, stream);
     if (e != cudaSuccess) return e;
-    // about 16 blocks per SM in all, but none without a piece of a whole page
+    // about 48 blocks per SM in all, but none without a piece of a whole page (the case above with
+    // its plan: 66 us with 8, 57 with 16, 50 with 48, 52 with 96)
     const long long page_bytes = pools.row_bytes << p.c.page_shift;
     const long long pieces = (page_bytes + kCopyBytes - 1) / kCopyBytes * pools.layers * 2;
-    long long each = ((long long)sms * 16 + p.n - 1) / p.n;
+    long long each = ((long long)sms * 48 + p.n - 1) / p.n;
     if (each > pieces) each = pieces;
     if (each > 65535) each = 65535;
     return launch_early(cache_tail_copy_kernel, dim3((unsigned)p.n, (unsigned)each), kCopyThreads, 0, stream, p, pools);
