@@ -389,21 +389,20 @@ __device__ CompactSlot compact_slot(const CompactParams& p, int s) {
     const int m = p.keep_lens[s];
     r.base = r.len - nodes;
     r.end = r.base + m;
-    bool bad = m < 0 || m > nodes;
+    // both checks read before either answers: their look-ups overlap
+    const bool range = m >= 0 && m <= nodes;
+    bool bad = !range, shared = false;
     const int* keep = p.keep + (size_t)s * p.T;
-    if (!bad) {
+    if (range) {
         for (int j = threadIdx.x; j < m; j += blockDim.x)
             bad |= keep[j] <= (j > 0 ? keep[j - 1] : -1) || keep[j] >= nodes;
-    }
-    bad = __syncthreads_or(bad);
-    bool shared = false;
-    if (!bad) {
         const int lo = r.base >> c.page_shift, hi = pages_of(r.end, c.page_shift);
         for (int j = lo + threadIdx.x; j < hi; j += blockDim.x) {
             const int page = row_of(c, s)[j];
             shared |= known(page, c) && __ldcg(c.refs + page) > 1;
         }
     }
+    bad = __syncthreads_or(bad);
     shared = __syncthreads_or(shared);
     r.status = bad ? GQA_CACHE_INVALID : (shared ? GQA_CACHE_SHARED : GQA_CACHE_DONE);
     return r;
@@ -411,11 +410,11 @@ __device__ CompactSlot compact_slot(const CompactParams& p, int s) {
 
 // Moves the accepted rows.  A thread owns one 16-byte column of one layer's K or V and walks
 // the accepted nodes in order: node keep[j] >= j goes to place j, so a row is overwritten only
-// after it was read, and eight rows may be read before their eight writes.  The rows' places are
+// after it was read, and sixteen rows may be read before their sixteen writes.  The rows' places are
 // looked up by the block together, kMoveRows at a time.  Bound by the latency of those look-ups and
 // two turns of reads: measured on B200, 73 MB (128 slots, trees of 64, 8 layers) in 16 us, 4.5 TB/s.
 constexpr int kMoveThreads = 128;
-constexpr int kMoveBatch = 8;
+constexpr int kMoveBatch = 16;
 constexpr int kMoveRows = 128;
 __global__ void __launch_bounds__(kMoveThreads) cache_compact_rows_kernel(const __grid_constant__ CompactParams p) {
     __shared__ int from_[kMoveRows], to_[kMoveRows];  // rows of a layer's pool; -1: not moved

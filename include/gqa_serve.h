@@ -97,7 +97,8 @@ GQA_API gqa_status gqa_attn_fwd_tree(const void* q, const void* k_cache, const v
  *   page_refs      [num_pages]: how many table entries name each page; 0 = the page is free.
  *                  Pages that the caller handles itself keep any other value (e.g. 1).
  *
- * page_size is a power of two >= 16.  Pages are taken lowest number first, for the requests
+ * Calls that read or change the same state are ordered by the caller, on one stream or with
+ * events.  page_size is a power of two >= 16.  Pages are taken lowest number first, for the requests
  * in their order: the outcome does not depend on scheduling.  Each request's outcome is
  * written to status[i] (device int32):
  */
