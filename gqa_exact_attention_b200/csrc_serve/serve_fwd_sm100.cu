@@ -90,13 +90,10 @@ struct Cfg {
     static constexpr int kSmemBytes = 1024 /* alignment slack */ + NT * kTileBytes + kSlots * kTileBytes +
                                       kOStageBytes + 8 * kNumBars + kStatsBytes + kPreBytes + 16 + kSegs * 128;
     static_assert(kSmemBytes * kCtasPerSm + 1024 * kCtasPerSm <= 233472, "shared memory per SM");
-    // of each 16 exponential pairs of an unmasked 32-key chunk, this many take the polynomial
-    // instead of the special-function unit
-#ifdef SERVE_POLY
-    static constexpr int kPolyPairs = SERVE_POLY;
-#else
+    // Of each 16 exponential pairs of an unmasked 32-key chunk, this many take the polynomial instead
+    // of the special-function unit.  Measured on B200 over 64 causal prompts: d = 64, 0 pairs 2.26 ms,
+    // 2 pairs 1.98, 3 pairs 1.92; d = 128, 0 and 2 pairs 1.63 ms, 4 pairs 1.70.
     static constexpr int kPolyPairs = HD == 128 ? 0 : 3;
-#endif
     static constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, false);
     static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, HD, true);
     __device__ static uint64_t sdesc(uint32_t saddr, uint32_t lbo) { return sdesc_sw128(saddr, lbo, 1024); }
@@ -672,10 +669,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
         tmem_relinquish();
         tc_fence_before();
     }
-    if constexpr (kRanges) {
-        let_next();
-        wait_before();
-    }
+    if constexpr (kRanges) wait_before();
     const long long* pre = p.pre;
     if constexpr (kRanges) {
         // the blocks of each sequence's units, summed up by every CTA for itself
@@ -687,6 +681,9 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // (the next kernel's CTAs come when every CTA here has its tensor memory: they never hold what
+    // one of these still waits for)
+    if constexpr (kRanges) let_next();
 
     // The next piece for this warp (its si-th), or NULL: none, or the CTA is aborting (ok false).
     auto next_piece = [&](uint32_t si, bool& ok) -> const Seg<NT>* {

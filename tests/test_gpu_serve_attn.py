@@ -466,3 +466,17 @@ def test_random_shapes_of_the_whole_range():
         lens = [int(x) for x in rng.integers(0, 1500, B)]
         run_tree(rng, lens, T, Hk * g, Hk, d, int(rng.choice([0, 16, 32, 128, 512])),
                  n=[int(x) for x in rng.integers(0, T + 2, B)] if rng.integers(2) else None, bf16=bool(rng.integers(2)))
+
+
+def test_more_sequences_than_a_cta_sums_up():
+    """Above 1024 sequences a kernel in front sums up the schedule: units that are split and units
+    that are not, prompts and trees."""
+    rng = np.random.default_rng(57)
+    lens = [0] * 2000
+    for b in rng.integers(0, 2000, 60):
+        lens[b] = int(rng.integers(1, 9))
+    run_varlen(rng, lens, lens, 4, 2, 64, True)
+    short = [int(x) for x in rng.integers(0, 40, 1100)]
+    run_tree(rng, short, 2, 2, 1, 64, 0)
+    run_tree(rng, short[:1090] + [700] * 10, 2, 2, 1, 64, 16)
+    run_tree(rng, short, 70, 2, 1, 64, 16)  # two tiles
