@@ -181,13 +181,19 @@ cudaMemPool_t workspace_pool(int dev) {
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
+        // the first call may be made in a stream capture, which otherwise forbids making a pool
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        cudaThreadExchangeStreamCaptureMode(&mode);
         cudaMemPool_t pool = nullptr;
-        if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) {
+        const bool made = cudaMemPoolCreate(&pool, &props) == cudaSuccess;
+        if (made) {
+            uint64_t keep = ~0ull;
+            cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        } else {
             cudaGetLastError();
-            return nullptr;
         }
-        uint64_t keep = ~0ull;
-        cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (!made) return nullptr;
         pools[dev] = pool;
     }
     return pools[dev];

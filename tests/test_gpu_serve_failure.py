@@ -1,5 +1,5 @@
 """Failure paths of the serving operators: a bounded wait that runs out, and scratch that cannot
-be had.  The wait runs out on purpose at a barrier that nothing completes (the GPU stays healthy);
+be had; and the first call of a process made in a stream capture.  The wait runs out on purpose at a barrier that nothing completes (the GPU stays healthy);
 each case runs in a process of its own."""
 import json
 import os
@@ -76,3 +76,43 @@ def test_waits_run_out_and_scratch_is_missing(kind):
     assert res["before"] == 0 and res["after"] == 0 and res["same"]
     assert res["stalled"] == 9 and res["seconds"] < 30
     assert res["alloc"] == 7 and res["untouched"]
+
+
+_FIRST = r"""
+import os, sys
+sys.path.insert(0, os.getcwd())
+import torch
+import gqa_exact_attention_b200 as G
+
+rn = lambda *s: torch.randn(s, device="cuda").bfloat16()
+ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+kind = sys.argv[1]
+if kind == "varlen":
+    q, k, v, cu = rn(3000, 32, 128), rn(3000, 8, 128), rn(3000, 8, 128), ints(0, 1000, 3000)
+    f = lambda: G.gqa_attn_fwd_varlen(q, k, v, cu, causal=True)
+elif kind == "tree":
+    q, k, v, mask, lens = rn(2, 8, 32, 128), rn(2, 4000, 8, 128), rn(2, 4000, 8, 128), ints(*[1] * 8).view(8, 1), ints(4000, 3000)
+    f = lambda: G.gqa_attn_fwd_tree(q, k, v, mask, lens)
+else:
+    table, lens, refs = ints(*[-1] * 32).view(4, 8), ints(0, 0, 0, 0), ints(*[0] * 40)
+    kp, vp, new, a, b = rn(2, 40, 16, 2, 64), rn(2, 40, 16, 2, 64), ints(20, 30, 0, 0), ints(0, 1), ints(2, 3)
+    f = lambda: (G.gqa_cache_resize(table, lens, refs, 16, new), G.gqa_cache_fork(kp, vp, table, lens, refs, a, b))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    x = f()
+graph.replay()
+torch.cuda.synchronize()
+y = f()
+torch.cuda.synchronize()
+assert all(torch.equal(s, t) for s, t in zip(x, y))
+print("SAME", flush=True)
+"""
+
+
+@pytest.mark.parametrize("kind", ["varlen", "tree", "cache"])
+def test_the_first_call_of_a_process_in_a_capture(kind):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    r = subprocess.run([sys.executable, "-c", _FIRST, kind], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert "SAME" in r.stdout, r.stdout + r.stderr
