@@ -8,7 +8,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdlib>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -50,22 +52,31 @@ int number(int64_t x, const char* name) {
     return (int)x;
 }
 
-// The stream argument: None (the current stream of the device) or a torch.cuda.Stream.
-void* stream_of(PyObject* o, int dev) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-    PyObject* x = PyObject_GetAttrString(o, "cuda_stream");
-    if (x == nullptr) {
-        PyErr_Clear();
-        refuse("stream must be a torch.cuda.Stream");
+// Makes the device current, and the stream argument's stream: None (the device's own current
+// one) or a torch.cuda.Stream.  Outputs are allocated with that stream current: a block that was
+// freed on another one may still be in use there.
+class On {
+public:
+    On(PyObject* o, int dev) : device_((c10::DeviceIndex)dev) {
+        if (o == Py_None) {
+            stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+            return;
+        }
+        PyObject* x = PyObject_GetAttrString(o, "cuda_stream");
+        stream = x != nullptr ? PyLong_AsVoidPtr(x) : nullptr;
+        Py_XDECREF(x);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            refuse("stream must be a torch.cuda.Stream");
+        }
+        given_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), (c10::DeviceIndex)dev));
     }
-    void* s = PyLong_AsVoidPtr(x);
-    Py_DECREF(x);
-    if (PyErr_Occurred()) {
-        PyErr_Clear();
-        refuse("stream must be a torch.cuda.Stream");
-    }
-    return s;
-}
+    void* stream = nullptr;
+
+private:
+    c10::cuda::CUDAGuard device_;
+    std::optional<c10::cuda::CUDAStreamGuard> given_;
+};
 
 double scale_of(PyObject* o, int64_t d) {
     if (o == Py_None) return 1.0 / std::sqrt((double)d);
@@ -178,12 +189,12 @@ PyObject* varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int* cqp = ints(cq, "cu_seqlens_q", {bounds}, dev);
         if (a[4] == Py_None && tk != tq) refuse("without cu_seqlens_k, k has as many rows as q");
         const int* ckp = a[4] == Py_None ? cqp : ints(a[4], "cu_seqlens_k", {bounds}, dev);
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const On on(a[10], dev);
         Outputs o = outputs(a[5], a[6], truth(a[7]), {tq, Hq, d}, {Hq, tq}, dev);
         const gqa_status st = gqa_attn_fwd_varlen(
             q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cqp, ckp, o.out.data_ptr(), o.code,
             static_cast<float*>(o.lse.data_ptr()), number(bounds - 1, "the batch"), number(tq, "q"), number(tk, "k"),
-            number(Hq, "Hq"), number(Hk, "Hk"), number(d, "d"), (float)scale_of(a[8], d), truth(a[9]), stream_of(a[10], dev));
+            number(Hq, "Hq"), number(Hk, "Hk"), number(d, "d"), (float)scale_of(a[8], d), truth(a[9]), on.stream);
         return failed(st) ? nullptr : pair(o.out, o.lse);
     });
 }
@@ -219,12 +230,12 @@ PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
             P = number(k.size(0), "the pool");
             page = number(k.size(1), "the page size");
         }
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const On on(a[11], dev);
         Outputs o = outputs(a[7], a[8], truth(a[9]), {B, T, Hq, d}, {B, Hq, T}, dev);
         const gqa_status st = gqa_attn_fwd_tree(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), table, M, P, page, lens, mp, shared, tl, o.out.data_ptr(), o.code,
             static_cast<float*>(o.lse.data_ptr()), number(B, "B"), number(T, "T"), Sk, number(Hq, "Hq"), number(Hk, "Hk"),
-            number(d, "d"), (float)scale_of(a[10], d), stream_of(a[11], dev));
+            number(d, "d"), (float)scale_of(a[10], d), on.stream);
         return failed(st) ? nullptr : pair(o.out, o.lse);
     });
 }
@@ -295,11 +306,11 @@ PyObject* resize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (a[5] == Py_None && m > s.S) refuse("without slots there are at most as many lengths as slots");
         const int* nl = ints(a[4], "new_lens", {m}, s.dev);
         const int* sl = ints_or_null(a[5], "slots", {m}, s.dev);
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)s.dev);
+        const On on(a[7], s.dev);
         at::Tensor st = status_of(a[6], m, s.dev);
         const gqa_status e = gqa_cache_resize(s.table, s.lens, s.refs, s.S, s.M, s.P, number(page < 0 ? 0 : page, "page_size"),
                                               sl, nl, number(m, "new_lens"), static_cast<int*>(st.data_ptr()),
-                                              stream_of(a[7], s.dev));
+                                              on.stream);
         return failed(e) ? nullptr : THPVariable_Wrap(st);
     });
 }
@@ -311,10 +322,10 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const PoolArgs p = pools(a, s);
         const int64_t m = tensor(a[5], "parents").numel();
         const int *pa = ints(a[5], "parents", {m}, s.dev), *ch = ints(a[6], "children", {m}, s.dev);
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)s.dev);
+        const On on(a[8], s.dev);
         at::Tensor st = status_of(a[7], m, s.dev);
         const gqa_status e = gqa_cache_fork(p.k, p.v, p.layers, p.row, s.table, s.lens, s.refs, s.S, s.M, s.P, p.page, pa, ch,
-                                            number(m, "parents"), static_cast<int*>(st.data_ptr()), stream_of(a[8], s.dev));
+                                            number(m, "parents"), static_cast<int*>(st.data_ptr()), on.stream);
         return failed(e) ? nullptr : THPVariable_Wrap(st);
     });
 }
@@ -329,11 +340,11 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t T = keep.size(1);
         const int *kp = ints(keep, "keep", {s.S, T}, s.dev), *kl = ints(a[6], "keep_lens", {s.S}, s.dev);
         const int* tl = ints_or_null(a[7], "tree_lens", {s.S}, s.dev);
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)s.dev);
+        const On on(a[9], s.dev);
         at::Tensor st = status_of(a[8], s.S, s.dev);
         const gqa_status e =
             gqa_cache_compact(p.k, p.v, p.layers, p.row, s.table, s.lens, s.refs, s.S, s.M, s.P, p.page, kp, kl, tl,
-                              number(T, "T"), static_cast<int*>(st.data_ptr()), stream_of(a[9], s.dev));
+                              number(T, "T"), static_cast<int*>(st.data_ptr()), on.stream);
         return failed(e) ? nullptr : THPVariable_Wrap(st);
     });
 }

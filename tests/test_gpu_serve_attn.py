@@ -480,3 +480,28 @@ def test_more_sequences_than_a_cta_sums_up():
     run_tree(rng, short, 2, 2, 1, 64, 0)
     run_tree(rng, short[:1090] + [700] * 10, 2, 2, 1, 64, 16)
     run_tree(rng, short, 70, 2, 1, 64, 16)  # two tiles
+
+
+def test_outputs_of_a_given_stream_come_from_its_memory():
+    """Memory freed on the current stream may still be in use there, so that a call on another
+    stream must not be given it for its outputs."""
+    rng = np.random.default_rng(57)
+    T, Hq = 5000, 8
+    a, b, c = (randn(rng, T, H, 64).cuda() for H in (Hq, 2, 2))
+    bounds = cu([T])
+    refs, lens = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    table, to = torch.full((2, 2), -1, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    x = G.gqa_attn_fwd_varlen(a, b, c, bounds)
+    st = G.gqa_cache_resize(table, lens, refs, 16, to)
+    torch.cuda.synchronize()
+    expect = [x[0].clone(), x[1].clone(), st.clone()]
+    s = torch.cuda.Stream()
+    was = [t.data_ptr() for t in (*x, st)]
+    del x, st  # the current stream has these to give
+    y = G.gqa_attn_fwd_varlen(a, b, c, bounds, stream=s)
+    st = G.gqa_cache_resize(table, lens, refs, 16, to, stream=s)
+    s.synchronize()
+    got = [*y, st]
+    assert all(torch.equal(p, q) for p, q in zip(expect, got))
+    assert not set(was) & {t.data_ptr() for t in got}
+    assert torch.cuda.current_stream() != s
