@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 const uint32_t d = tmem + C::s_col(t);
                 bool ready = false;
                 if (elect_one()) {
-                    // 32 bytes of the row per MMA: 16 bf16 or 32 e4m3 of d
+                    // 32 bytes of the row per MMA: 16 elements of d
                     constexpr int kSteps = C::kRowBytes / 32;
 #pragma unroll
                     for (int kk = 0; kk < kSteps; ++kk) {

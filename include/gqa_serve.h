@@ -75,7 +75,8 @@ GQA_API gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, co
  *   out, lse        [B, T, Hq, d] and [B, Hq, T].  A row that sees no key, and rows i >= n_b,
  *                   get out = 0 and lse = -inf.
  *
- * Keys at or past L_b do not reach the result, whatever they hold.  A table entry outside
+ * Keys at or past L_b do not reach the result, whatever they hold.  A value of V before L_b
+ * that is not finite reaches every row of its 128-key block, as in gqa_attn_fwd.  A table entry outside
  * [0, num_pages) reads as a page of zeros.  Errors as gqa_attn_fwd_paged; GQA_ERR_NULL for a
  * NULL tree_mask or cache_seqlens, GQA_ERR_ALIGN for an int32 pointer that is not 4-byte
  * aligned.
