@@ -8,7 +8,7 @@
 // cluster barriers (a fraction of a microsecond) instead of launches, and the state stays in
 // L2.  Nothing depends on the order in which atomics land: the counts only add up.  What a call
 // costs is latency, the dependent reads of its steps (lengths, table entries, counts): measured on
-// B200, 4 us for 8 slots of a small cache, 21 us for 256 slots over 131 thousand pages, whose bytes
+// B200, 4 us for 8 slots of a small cache, 20 us for 256 slots over 131 thousand pages, whose bytes
 // alone would take 1 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -237,6 +237,15 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(const __grid_const
         for (int e = 0; e < kFew; ++e) m |= x[e] == 0 ? 1u << e : 0u;
         return m;
     };
+    // the first request of lo..hi with upto > r (one has)
+    auto first_past = [&](int r, int lo, int hi) {
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (upto[mid] > r) hi = mid;
+            else lo = mid + 1;
+        }
+        return lo;
+    };
     if (needed > 0) {
         sync();  // the counts are final
         int mine = 0;
@@ -275,17 +284,18 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(const __grid_const
                 if (lane >= o) upto_group += y;
             }
             const int in_group = upto_group - __popc(group);
+            const int here = __shfl_sync(0xffffffffu, upto_group, 31);
+            if (here == 0) continue;
+            // the requests that these pages go to: few, where requests take many pages
+            const int end = min(free_before + here, needed) - 1;
+            const int found = first_past(lane == 0 ? free_before : end, 0, n - 1);
+            const int req_lo = __shfl_sync(0xffffffffu, found, 0), req_hi = __shfl_sync(0xffffffffu, found, 1);
             while (__any_sync(0xffffffffu, m != 0u)) {  // every lane's next page
                 const int e = m != 0u ? __ffs(m) - 1 : 0;
                 const unsigned others = __shfl_sync(0xffffffffu, group, e);
                 const int r = free_before + __shfl_sync(0xffffffffu, in_group, e) + __popc(others & ((1u << lane) - 1u));
                 if (m != 0u && r < needed) {
-                    int lo = 0, hi = n - 1;  // the first request with upto > r
-                    while (lo < hi) {
-                        const int mid = (lo + hi) >> 1;
-                        if (upto[mid] > r) hi = mid;
-                        else lo = mid + 1;
-                    }
+                    const int lo = first_past(r, req_lo, req_hi);
                     const int entry = first[lo] + (r - (lo > 0 ? upto[lo - 1] : 0));
                     if (upto[lo] <= free_all && entry < c.M) {
                         const int page = at + e * 32 + lane;
@@ -295,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) cache_plan_kernel(const __grid_const
                 }
                 m &= m - 1u;
             }
-            free_before += __shfl_sync(0xffffffffu, upto_group, 31);
+            free_before += here;
         }
     }
 
@@ -486,7 +496,7 @@ __global__ void __launch_bounds__(128) cache_compact_pages_kernel(const __grid_c
 
 // Blocks of the cluster: a block for every 1024 pages of the pool or 8 warp turns of table entries,
 // at most 16; one for a small cache, whose steps then need no cluster barrier.  Measured on B200
-// with the calls around them: 131 thousand pages and 256 slots of 2048 entries, 21 us a call (25 with
+// with the calls around them: 131 thousand pages and 256 slots of 2048 entries, 20 us a call (25 with
 // 8 blocks of twice the threads); 4 thousand pages and 128 slots, a verification step of 34 us
 // (39 with a block for every 8192 pages).
 int plan_ctas(const PlanParams& p) {
