@@ -129,6 +129,28 @@ __device__ __forceinline__ void exp2_poly4(float x0, float x1, float& y0, float&
     y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
+// Three- and two-input extrema that are NaN where an input is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 template <uint32_t R>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -419,10 +441,11 @@ template <int HD, int NT, int MODE, bool PART>
 __device__ __forceinline__ void write_row(const ServeParams& p, uint32_t o_addr, const RowMap& rm, const Seg<NT>& g,
                                           int t, int row, bool has, bool idle, bool valid, float m, float l,
                                           uint32_t o_empty_bar) {
-    const float inv_l = l > 0.f ? 1.f / l : 0.f;
-    const float lse2 = l > 0.f && valid ? m + __log2f(l) : -INFINITY;
+    // (no key: 0, whatever V holds; a NaN sum is not 0)
+    const bool zero = !has || !valid || l == 0.f;
+    const float inv_l = zero ? 0.f : 1.f / l;
+    const float lse2 = zero ? -INFINITY : m + __log2f(l);
     const size_t at = PART ? 0 : out_row<MODE>(p, g.b, g.s, rm) * HD;
-    const bool zero = !has || !valid || l == 0.f;  // (no key: 0, whatever V holds)
 #pragma unroll
     for (int ch = 0; ch < HD / 32; ++ch) {
         uint32_t r[32];
@@ -447,7 +470,7 @@ __device__ __forceinline__ void write_row(const ServeParams& p, uint32_t o_addr,
 #pragma unroll
                 for (int i = 0; i < 32; ++i) r[i] = 0u;
             }
-            store_cols<4>(p, at + ch * 32, reinterpret_cast<const float(&)[32]>(r), zero ? 0.f : inv_l);
+            store_cols<4>(p, at + ch * 32, reinterpret_cast<const float(&)[32]>(r), inv_l);
         }
     }
     if (rm.ok) {
@@ -1324,12 +1347,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 };
                 float e[1];
                 if (c >= 0.f)
-                    e[0] = extremum([](float x, float y, float z) { return max3(x, y, z); },
-                                    [](float x, float y) { return fmaxf(x, y); });
+                    e[0] = extremum([](float x, float y, float z) { return max_nan(x, y, z); },
+                                    [](float x, float y) { return max_nan(x, y); });
                 else
-                    e[0] = extremum([](float x, float y, float z) { return min3(x, y, z); },
-                                    [](float x, float y) { return fminf(x, y); });
-                const float mx = nothing ? kNegInf : (c == 0.f ? 0.f : e[0] * c);
+                    e[0] = extremum([](float x, float y, float z) { return min_nan(x, y, z); },
+                                    [](float x, float y) { return min_nan(x, y); });
+                const float mx = nothing ? kNegInf : e[0] * c;
                 // Reference max m (log2 units): the max of the row's first block with a key, exactly
                 // (so that the largest weight is 1 and a row with one key gives its value back), then
                 // moved only when a block's max passes m + 8, which keeps every p <= 256 and spares
@@ -1343,8 +1366,12 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 }
                 // P = 2^(c*s - m) as bf16, written over S in TMEM (S is in registers).  A
                 // disallowed key gets the exponent -inf, i.e. p = 0, for any sign of c.
-                const float neg_m = -m;
-                float ls0 = 0.f, ls1 = 0.f;
+                // Scores that are not finite: one that is NaN or +inf makes the row's sum NaN, and
+                // by it the row's output and LSE (the exponentials alone would not: the polynomial's
+                // exponent bits turn a NaN into a number).  -inf is a weight of 0 (2^-126 in the
+                // polynomial), and while a row has seen nothing else m stays -inf: 0 in its place.
+                const float neg_m = m == kNegInf ? 0.f : -m;
+                float ls0 = mx < INFINITY ? 0.f : NAN, ls1 = 0.f;
                 // One 32-key chunk: P = 2^(c s - m) as 16 columns of bf16 pairs; with kSelect, keys
                 // that the row does not see get the exponent -inf (p = 0 for either sign of c).
                 // bf16 is the matrix unit's input: the sum keeps the unrounded p.
@@ -1429,6 +1456,7 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                 mbar_arrive(p_full(t));
             }
             if (!ok) break;
+            if (m == kNegInf) l *= 0.f;  // scores of -inf only: no key (and NaN stays)
             if constexpr (C::kEpilogueWG) {
                 // row statistics for the epilogue warpgroup (double-buffered by unit)
                 float* st = stats + ((stn & 1u) * NT + t) * 256;
@@ -1494,9 +1522,10 @@ __global__ void __launch_bounds__(Cfg<HD, NT, MODE != kVarlenList>::kThreads, Cf
                     write_row<HD, NT, MODE, true>(p, o_addr, rm, g, t, row, has, idle, valid, m, l, o_empty(t));
                     continue;
                 }
-                const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
-                const float lse_v = (l > 0.f && valid) ? (m + __log2f(l)) * kLn2 : -INFINITY;
-                const bool zero = !has || idle || !valid || l == 0.f;  // (no key: 0, whatever V holds)
+                // (no key: 0, whatever V holds; a NaN sum is not 0)
+                const bool zero = !has || idle || !valid || l == 0.f;
+                const float inv_l = zero ? 0.f : 1.f / l;
+                const float lse_v = zero ? -INFINITY : (m + __log2f(l)) * kLn2;
                 // A stage row is 128 bytes: 32 fp32 or 64 bf16 columns.  A full tile leaves by a TMA
                 // store; in a tile that the sequence's end cuts, the rows behind it belong to the
                 // next sequence, and its own are stored one by one.  (A tree's tiles end where the
@@ -1635,7 +1664,8 @@ __global__ void __launch_bounds__(kJoinThreads) serve_join_kernel(const __grid_c
 #pragma unroll
                 for (int a = 0; a < kAhead; ++a) {
                     const float li = i0 + a < u.parts ? lse_of(i0 + a, t, row) : -INFINITY;
-                    w[a] = li > -INFINITY ? ex2_approx(li - M) : 0.f;  // 0: no keys, and nothing was written
+                    // 0: no keys, and nothing was written.  A NaN sum passes through as NaN.
+                    w[a] = li == -INFINITY ? 0.f : ex2_approx(li - M);
                 }
 #pragma unroll
                 for (int a = 0; a < kAhead; ++a)
@@ -1653,8 +1683,8 @@ __global__ void __launch_bounds__(kJoinThreads) serve_join_kernel(const __grid_c
                     }
                 }
             }
-            store_cols<kWide>(p, out_row<MODE>(p, u.b, s, rm) * HD + col * 8 * kWide, acc, sum > 0.f ? 1.f / sum : 0.f);
-            if (col == 0) p.lse[lse_row<MODE>(p, u.b, s, rm)] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+            store_cols<kWide>(p, out_row<MODE>(p, u.b, s, rm) * HD + col * 8 * kWide, acc, sum == 0.f ? 0.f : 1.f / sum);
+            if (col == 0) p.lse[lse_row<MODE>(p, u.b, s, rm)] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * kLn2;
         }
     };
     using W = std::integral_constant<int, 4>;

@@ -40,8 +40,9 @@ extern "C" {
  *   lse  fp32 [Hq, total_q].  Rows that belong to no sequence are left as they were, in both.
  *
  * What other sequences hold does not reach a sequence's result, not even infinities or NaN.
- * Within a sequence a value of V that is not finite reaches every row of its 128-key block,
- * as in gqa_attn_fwd.
+ * Within a sequence, a row that sees a key whose score is NaN or +inf gets NaN in out and lse; a
+ * score of -inf weighs nothing, and a row all of whose scores are -inf is one that sees no key.
+ * A value of V that is not finite reaches every row of its 128-key block, as in gqa_attn_fwd.
  *
  * total_q = 0 returns GQA_OK and does nothing; total_k = 0 is a batch without keys (k and v
  * may be NULL).  Errors as gqa_attn_fwd; GQA_ERR_SHAPE also for a stride that is not
@@ -75,8 +76,8 @@ GQA_API gqa_status gqa_attn_fwd_varlen(const void* q, long long q_row_stride, co
  *   out, lse        [B, T, Hq, d] and [B, Hq, T].  A row that sees no key, and rows i >= n_b,
  *                   get out = 0 and lse = -inf.
  *
- * Keys at or past L_b do not reach the result, whatever they hold.  A value of V before L_b
- * that is not finite reaches every row of its 128-key block, as in gqa_attn_fwd.  A table entry outside
+ * Keys at or past L_b do not reach the result, whatever they hold.  Scores and values of V
+ * before L_b that are not finite count as in gqa_attn_fwd_varlen.  A table entry outside
  * [0, num_pages) reads as a page of zeros.  Errors as gqa_attn_fwd_paged; GQA_ERR_NULL for a
  * NULL tree_mask or cache_seqlens, GQA_ERR_ALIGN for an int32 pointer that is not 4-byte
  * aligned.
