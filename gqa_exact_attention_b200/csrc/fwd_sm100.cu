@@ -237,6 +237,10 @@ __device__ __forceinline__ RowMap row_map(const FwdParams& p, int pos0, int hg, 
     return m;
 }
 
+// A row whose sum is below this has seen no key, or only scores of -inf (weights of 0, or of 2^-126
+// where the polynomial clamps): the largest weight of any other score is at least 2^-64.
+constexpr float kNothing = 0x1p-100f;
+
 // Writes one tile row's output: O / l from TMEM (or zeros for a tile with no key in this
 // split) and LSE = (m + log2 l) ln 2, to out/lse or to the split partials.  Arrives on
 // o_empty once O is in registers, so the next unit's PV may overwrite it.
@@ -245,8 +249,9 @@ __device__ __forceinline__ void write_row(const FwdParams& p, uint32_t o_addr, c
                                           int b, int split, bool has, bool idle, float m, float l,
                                           uint32_t o_empty_bar) {
     constexpr float kLn2 = 0.69314718055994530942f;
-    const float inv_l = (l > 0.f) ? p.v_scale / l : 0.f;
-    const float lse_v = (l > 0.f) ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    // (a NaN sum is not nothing)
+    const float inv_l = l < kNothing ? 0.f : p.v_scale / l;
+    const float lse_v = l < kNothing ? -INFINITY : (m + __log2f(l)) * kLn2;
     float* orow = nullptr;
     float* lrow;
     uint16_t* bf16_row = nullptr;  // bf16 output row (final output only)
@@ -942,12 +947,12 @@ __global__ void __launch_bounds__(FwdCfg<HD, NT, F8>::kThreads, FwdCfg<HD, NT, F
                 };
                 float e[1];
                 if (c >= 0.f)
-                    e[0] = extremum([](float x, float y, float z) { return max3(x, y, z); },
-                                    [](float x, float y) { return fmaxf(x, y); });
+                    e[0] = extremum([](float x, float y, float z) { return max_nan(x, y, z); },
+                                    [](float x, float y) { return max_nan(x, y); });
                 else
-                    e[0] = extremum([](float x, float y, float z) { return min3(x, y, z); },
-                                    [](float x, float y) { return fminf(x, y); });
-                const float mx = (lim <= 0) ? kNegInf : (c == 0.f ? 0.f : e[0] * c);
+                    e[0] = extremum([](float x, float y, float z) { return min_nan(x, y, z); },
+                                    [](float x, float y) { return min_nan(x, y); });
+                const float mx = (lim <= 0) ? kNegInf : e[0] * c;
                 // Reference max m (log2 units).  It starts at 0, not at the row's first
                 // block max, and moves only when a block's max leaves the window [m - 64,
                 // m + 8]: up past m + 8 (deferred rescaling, which keeps every p <= 256),
@@ -965,14 +970,18 @@ __global__ void __launch_bounds__(FwdCfg<HD, NT, F8>::kThreads, FwdCfg<HD, NT, F
                 // still by integers, and e4m3 rounding commutes with powers of two.
                 constexpr float kLowEdge = F8 ? 1.0f : 64.f;
                 constexpr float kHeadroom = F8 ? 4.0f : 0.f;
-                const bool grow = mx > m + 8.0f || (l == 0.f && mx > kNegInf && mx < m - kLowEdge);
+                const bool grow = mx > m + 8.0f || (l < kNothing && mx > kNegInf && mx < m - kLowEdge);
                 float alpha = 1.f;
                 if (grow) {
                     const float m_new = ceilf(mx) - kHeadroom;
-                    alpha = (l == 0.f) ? 0.f : ex2_approx(m - m_new);  // nothing summed: O is 0
+                    alpha = l < kNothing ? 0.f : ex2_approx(m - m_new);  // nothing summed: O is 0
                     l *= alpha;
                     m = m_new;
                 }
+                // A score that is NaN or +inf makes the row's sum NaN, and by it the row's output
+                // and LSE (the exponentials alone would not: the polynomial's exponent bits turn
+                // a NaN into a number).
+                if (!(mx < INFINITY)) l = NAN;
                 // P = 2^(c*s - m) as bf16, written over S in TMEM (S is in registers).  A
                 // disallowed key gets the exponent -inf, i.e. p = 0, for any sign of c.
                 const float neg_m = -m;
@@ -1131,8 +1140,8 @@ __global__ void __launch_bounds__(FwdCfg<HD, NT, F8>::kThreads, FwdCfg<HD, NT, F
                 ok = named_bar_and(kEpiBar, 128, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float inv_l = (l > 0.f) ? p.v_scale / l : 0.f;
-                const float lse_v = (l > 0.f) ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                const float inv_l = l < kNothing ? 0.f : p.v_scale / l;
+                const float lse_v = l < kNothing ? -INFINITY : (m + __log2f(l)) * kLn2;
                 const uint32_t o_addr = tmem + ((uint32_t)(quarter * 32) << 16) + C::o_col(t);
                 const int hcoord = p.pack ? g.hg * p.g : g.hg;
                 const int bcoord = p.num_splits == 1 ? g.b : g.split * p.B + g.b;
@@ -1322,7 +1331,7 @@ __global__ void __launch_bounds__(1024) gqa_unit_order_kernel(const __grid_const
 
 // ---------------------------------------------------------------- split-KV combine
 // One warp per output row (b, h, i): M = max_s lse_s, w_s = exp(lse_s - M),
-// lse = M + ln sum w_s, O = sum_s w_s O_s / sum_s w_s.
+// lse = M + ln sum w_s, O = sum_s w_s O_s / sum_s w_s.  A partial's NaN stays one.
 template <int HD>
 __global__ void __launch_bounds__(256) gqa_combine_kernel(const CombineParams p) {
     constexpr int kPer = HD / 32;
@@ -1336,7 +1345,7 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const CombineParams p)
         float M = ls;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float w = (M == kNegInf || ls == kNegInf) ? 0.f : __expf(ls - M);
+        float w = ls == kNegInf ? 0.f : __expf(ls - M);
         float wsum = w;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
@@ -1363,7 +1372,7 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const CombineParams p)
                 acc[1] += ws * v.y;
             }
         }
-        const float inv = (wsum > 0.f) ? 1.f / wsum : 0.f;
+        const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
         // r = (b * Hq + h) * Sq + i  ->  out[b, i, h, :]
         const long long i = r % p.Sq;
         const long long bh = r / p.Sq;
@@ -1387,7 +1396,7 @@ __global__ void __launch_bounds__(256) gqa_combine_kernel(const CombineParams p)
                 *reinterpret_cast<float2*>(dst) = make_float2(acc[0] * inv, acc[1] * inv);
             }
         }
-        if (lane == 0) p.lse[r] = (wsum > 0.f) ? M + __logf(wsum) : kNegInf;
+        if (lane == 0) p.lse[r] = wsum == 0.f ? kNegInf : M + __logf(wsum);
     }
 }
 

@@ -380,15 +380,25 @@ __device__ __forceinline__ void add2(float a0, float a1, float b0, float b1, flo
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// three-input extrema (sm_100)
-__device__ __forceinline__ float max3(float a, float b, float c) {
+// three- and two-input extrema, NaN where an input is (three inputs: sm_100)
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
+__device__ __forceinline__ float max_nan(float a, float b) {
     float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 
