@@ -67,9 +67,8 @@ def _compile(lib, folders, files, verbose):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile each library if any of its sources is newer than it; return the forward's path."""
-    build_serve(force, verbose)
-    build_bind(force)
+    """Compile the forward's library if any source is newer than it (nvcc alone is needed); return
+    its path."""
     if not force and not _stale():
         return LIB
     return _compile(LIB, [CSRC], sources(), verbose)
@@ -102,5 +101,12 @@ def build_bind(force: bool = False) -> str:
     return SERVE_BIND
 
 
+def build_all(force: bool = False, verbose: bool = False) -> None:
+    """The forward's library, the serving library and, with torch, the latter's binding."""
+    build(force, verbose)
+    build_serve(force, verbose)
+    build_bind(force)
+
+
 if __name__ == "__main__":
-    build(force=True, verbose=True)
+    build_all(force=True, verbose=True)

@@ -1,0 +1,47 @@
+"""The in-tree builds on the host: what each needs, what a failed one does, and when one is stale.
+Nothing is compiled: the compilers are replaced by a record of their commands."""
+import importlib.util
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+_WITHOUT_TORCH = r"""
+import sys
+sys.modules["torch"] = None  # import torch raises ImportError
+import gqa_exact_attention_b200 as G
+from gqa_exact_attention_b200 import _build
+built = []
+_build.subprocess.run = lambda cmd, **kw: built.append(cmd[cmd.index("-o") + 1])
+_build._older = lambda lib, deps: True
+_build.build()
+assert built == [_build.LIB], built
+G._have_nvcc = lambda: True
+G.load()
+assert built == [_build.LIB] * 2, built
+print("built")
+"""
+
+
+def test_the_forward_builds_and_loads_without_torch():
+    r = subprocess.run([sys.executable, "-c", _WITHOUT_TORCH], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.split() == ["built"], r.stderr
+
+
+@pytest.fixture
+def build(monkeypatch):
+    """A fresh copy of the build module that only records its commands."""
+    spec = importlib.util.spec_from_file_location("gqa_build_copy", os.path.join(ROOT, "gqa_exact_attention_b200", "_build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.commands = []
+    monkeypatch.setattr(mod, "subprocess", type("Record", (), {"run": staticmethod(lambda cmd, **kw: mod.commands.append(cmd))}))
+    return mod
+
+
+def test_build_all_builds_the_binding_after_its_library(build):
+    build.build_all(force=True)
+    assert [c[c.index("-o") + 1] for c in build.commands] == [build.LIB, build.SERVE_LIB, build.SERVE_BIND]
