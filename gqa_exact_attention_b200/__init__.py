@@ -76,15 +76,8 @@ def load():
     global _lib
     if _lib is not None:
         return _lib
-    try:
-        from . import _build
-        if _build._stale() and _have_nvcc():
-            _build.build()
-    except Exception as e:  # a failed build must not hide behind an old library
-        if not os.path.exists(lib_path):
-            raise RuntimeError(f"libgqa_attn.so is missing and could not be built: {e}") from e
-    if not os.path.exists(lib_path):
-        raise RuntimeError(f"libgqa_attn.so not found at {lib_path}; run the package build")
+    from . import _build
+    _rebuild("libgqa_attn.so", lib_path, _build._stale, _build.build, _have_nvcc())
     L = ctypes.CDLL(lib_path)
     i, f, p, sz = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
     L.gqa_attn_fwd.argtypes = [p, p, p, p, p, i, i, i, i, i, i, f, i, i, i, p]
@@ -107,6 +100,18 @@ def load():
     L.gqa_attn_fwd_fp8.restype = i
     _lib = L
     return L
+
+
+def _rebuild(name, path, stale, build, compiler):
+    """Build what is absent or older than its sources, where there is a compiler.  A build that
+    fails raises: an old library must not stand in for it."""
+    if compiler and stale():
+        try:
+            build()
+        except Exception as e:
+            raise RuntimeError(f"{name} is missing or older than its sources, and could not be built: {e}") from e
+    if not os.path.exists(path):
+        raise RuntimeError(f"{name} not found at {path}; run the package build")
 
 
 def _have_nvcc() -> bool:

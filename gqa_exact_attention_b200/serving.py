@@ -11,8 +11,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+from shutil import which
 
-from . import _check, _have_nvcc, _range
+from . import _check, _have_nvcc, _range, _rebuild
 
 __all__ = [
     "gqa_attn_fwd_varlen", "gqa_attn_fwd_tree", "gqa_cache_resize", "gqa_cache_fork",
@@ -40,17 +41,8 @@ def load_serve():
     global _lib
     if _lib is not None:
         return _lib
-    try:
-        from . import _build
-        if _build.serve_stale() and _have_nvcc():
-            _build.build_serve()
-        if _build.bind_stale() and _have_nvcc():
-            _build.build_bind()
-    except Exception as e:  # a failed build must not hide behind an old library
-        if not os.path.exists(serve_lib_path):
-            raise RuntimeError(f"libgqa_serve.so is missing and could not be built: {e}") from e
-    if not os.path.exists(serve_lib_path):
-        raise RuntimeError(f"libgqa_serve.so not found at {serve_lib_path}; run the package build")
+    from . import _build
+    _rebuild("libgqa_serve.so", serve_lib_path, _build.serve_stale, _build.build_serve, _have_nvcc())
     L = ctypes.CDLL(serve_lib_path)
     i, f, p, ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
     L.gqa_attn_fwd_varlen.argtypes = [p, ll, p, ll, p, ll, p, p, p, i, p, i, i, i, i, i, i, f, i, p]
@@ -76,6 +68,8 @@ def _load_bind():
     load_serve()
     import torch  # noqa: F401  (the module's own libraries)
 
+    from . import _build
+    _rebuild("_serve_bind.so", _build.SERVE_BIND, _build.bind_stale, _build.build_bind, which("g++") is not None)
     from . import _serve_bind
     _serve_bind.on_error(_check)
     _bind = _serve_bind

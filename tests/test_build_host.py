@@ -45,3 +45,32 @@ def build(monkeypatch):
 def test_build_all_builds_the_binding_after_its_library(build):
     build.build_all(force=True)
     assert [c[c.index("-o") + 1] for c in build.commands] == [build.LIB, build.SERVE_LIB, build.SERVE_BIND]
+
+
+_FAILING = r"""
+import subprocess, sys
+import gqa_exact_attention_b200 as G
+from gqa_exact_attention_b200 import _build, serving
+G._have_nvcc = serving._have_nvcc = lambda: True
+def run(cmd, **kw):
+    raise subprocess.CalledProcessError(1, cmd)
+_build.subprocess = type("S", (), {"run": staticmethod(run)})
+which, stale = sys.argv[1:]
+real = _build._older
+_build._older = lambda lib, deps: lib.endswith(stale) or real(lib, deps)
+try:
+    {"forward": G.load, "serving": G.load_serve, "binding": serving._load_bind}[which]()
+    print("loaded")
+except RuntimeError as e:
+    print("refused", stale in str(e))
+"""
+
+
+@pytest.mark.parametrize("which,stale,want", [
+    ("forward", "libgqa_attn.so", "refused True"), ("serving", "libgqa_serve.so", "refused True"),
+    ("binding", "_serve_bind.so", "refused True"), ("binding", "libgqa_serve.so", "refused True"),
+    ("forward", "_serve_bind.so", "loaded"), ("serving", "_serve_bind.so", "loaded")])
+def test_a_failed_build_does_not_hide_behind_an_old_library(which, stale, want):
+    pytest.importorskip("torch")
+    r = subprocess.run([sys.executable, "-c", _FAILING, which, stale], cwd=ROOT, capture_output=True, text=True)
+    assert r.stdout.strip() == want, r.stdout + r.stderr
