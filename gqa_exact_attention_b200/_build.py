@@ -5,6 +5,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -46,7 +47,22 @@ def serve_stale() -> bool:
 
 
 def bind_stale() -> bool:
-    return _older(SERVE_BIND, [SERVE_BIND_SRC])
+    return _older(SERVE_BIND, [SERVE_BIND_SRC]) or _bind_made_for() != _bind_abi()
+
+
+def _bind_abi() -> str:
+    """What the binding is compiled against."""
+    import torch
+    return f"{sys.implementation.cache_tag} torch {torch.__version__}"
+
+
+def _bind_made_for():
+    # written beside the module once it is built
+    try:
+        with open(SERVE_BIND + ".stamp") as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def _older(lib, deps) -> bool:
@@ -97,7 +113,11 @@ def build_bind(force: bool = False) -> str:
         cmd += ["-isystem", p]
     cmd += [SERVE_BIND_SRC, "-o", SERVE_BIND, "-L", HERE, "-l:libgqa_serve.so", "-Wl,-rpath,$ORIGIN",
             "-L", libs, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"]
+    if os.path.exists(SERVE_BIND + ".stamp"):
+        os.remove(SERVE_BIND + ".stamp")
     subprocess.run(cmd, check=True)
+    with open(SERVE_BIND + ".stamp", "w") as f:
+        f.write(_bind_abi())
     return SERVE_BIND
 
 

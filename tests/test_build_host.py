@@ -74,3 +74,36 @@ def test_a_failed_build_does_not_hide_behind_an_old_library(which, stale, want):
     pytest.importorskip("torch")
     r = subprocess.run([sys.executable, "-c", _FAILING, which, stale], cwd=ROOT, capture_output=True, text=True)
     assert r.stdout.strip() == want, r.stdout + r.stderr
+
+
+def test_a_binding_built_for_another_torch_is_stale(build, tmp_path, monkeypatch):
+    torch = pytest.importorskip("torch")
+    so = tmp_path / "_serve_bind.so"
+    monkeypatch.setattr(build, "SERVE_BIND", str(so))
+
+    def run(cmd, **kw):
+        so.write_bytes(b"")
+    monkeypatch.setattr(build.subprocess, "run", staticmethod(run))
+    assert build.bind_stale()
+    build.build_bind()
+    assert not build.bind_stale()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert build.bind_stale()
+    build.build_bind()
+    assert not build.bind_stale()
+    monkeypatch.setattr(build.sys.implementation, "cache_tag", "cpython-300")
+    assert build.bind_stale()
+
+
+def test_a_failed_build_of_the_binding_leaves_it_stale(build, tmp_path, monkeypatch):
+    pytest.importorskip("torch")
+    so = tmp_path / "_serve_bind.so"
+    monkeypatch.setattr(build, "SERVE_BIND", str(so))
+
+    def run(cmd, **kw):
+        so.write_bytes(b"")  # (some of it)
+        raise OSError("no space")
+    monkeypatch.setattr(build.subprocess, "run", staticmethod(run))
+    with pytest.raises(OSError):
+        build.build_bind()
+    assert build.bind_stale()
