@@ -1699,16 +1699,36 @@ __global__ void __launch_bounds__(1024) serve_list_kernel(const __grid_constant_
         *lo = min(max(fresh(cu + b), 0), total);
         *n = min(max(fresh(cu + b + 1), *lo), total) - *lo;
     };
+    auto start = [&](int b) { return min(max(fresh(p.cu_q + b), 0), p.total_q); };
+    bool back = false;
     for (int b = tid; b < p.B; b += 1024) {
         int k0, sk;
         bounds(p.cu_k, b, p.total_k, &k0, &sk);
         atomicMax(&most, (sk + kServeBlockN - 1) / kServeBlockN);
+        back |= start(b + 1) < start(b);
     }
-    __syncthreads();
+    // Where bounds decrease, a sequence that starts before the end of an earlier one is left out:
+    // its rows are unspecified, and the groups of the others fit the list and leave no row out.
+    const bool tangled = __syncthreads_or(back) != 0;
     const int per_bucket = (most + kServeBuckets - 1) / kServeBuckets;
     // a warp per sequence, a lane per tile group
     auto each = [&](auto f) {
-        for (int b = warp; b < p.B; b += 32) {
+        int reach = 0;  // (tangled) the largest bound so far
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + warp;
+            if (tangled) {
+                int x = b0 + lane < p.B ? start(b0 + lane) : 0;
+                const int mine = __shfl_sync(0xffffffffu, x, warp);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x = max(x, y);
+                }
+                const bool in_order = mine >= max(reach, __shfl_sync(0xffffffffu, x, warp));
+                reach = max(reach, __shfl_sync(0xffffffffu, x, 31));
+                if (!in_order) continue;
+            }
+            if (b >= p.B) break;
             int q0, lq, k0, sk;
             bounds(p.cu_q, b, p.total_q, &q0, &lq);
             bounds(p.cu_k, b, p.total_k, &k0, &sk);
@@ -1755,7 +1775,7 @@ __global__ void __launch_bounds__(1024) serve_list_kernel(const __grid_constant_
         base += own[j];
     }
     __syncthreads();
-    // (sequences that overlap could have more groups than the list has room for)
+    // (the list has room for them all: the sequences are apart)
     each([&](int key, int b, int mt) {
         const int at = atomicAdd(&count[key], 1);
         if (at < p.list_cap) p.list[at] = make_int2(b, mt);

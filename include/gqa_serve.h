@@ -32,8 +32,9 @@ extern "C" {
  *   cu_seqlens_q, cu_seqlens_k   device int32 [B + 1]: sequence b has query rows
  *        [cu_seqlens_q[b], cu_seqlens_q[b+1]) and key rows [cu_seqlens_k[b],
  *        cu_seqlens_k[b+1]).  They start at any value >= 0 and do not decrease; bounds
- *        outside [0, total] are clamped to it.  Sequences that overlap or decrease give
- *        unspecified values in the rows of out and lse that they cover, and nothing else.
+ *        outside [0, total] are clamped to it.  Where they decrease, a sequence that starts
+ *        before the end of an earlier one gives unspecified values in the rows of out and lse
+ *        that it covers, and nothing else.
  *   causal   bottom-right aligned in each sequence: with Lq queries and Lk keys, query i
  *        sees key j iff j <= i + Lk - Lq.  A row that sees no key gets out = 0, lse = -inf.
  *   out  fp32 or bf16 [total_q, Hq, d] (out_dtype as in gqa_attn_fwd_kvcache).
