@@ -37,6 +37,7 @@
 #include "launch_serve.h"
 #include "ptx_sm100.cuh"
 #include "serve_params.h"
+#include "serve_ranges.h"
 
 namespace gqa {
 
@@ -199,22 +200,6 @@ struct Walk {
     int b;
     ServeBound bound;  // ranges: the unit of the first piece
 };
-// floor(a * b / c): 64-bit division is slow, and rarely needed
-__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
-    const long long ab = a * b;
-    if ((unsigned long long)ab < (1ull << 32) && c < (1ll << 32)) return (uint32_t)ab / (uint32_t)c;
-    return ab / c;
-}
-__device__ __forceinline__ long long range_start(const Walk& w, int cta) { return mul_div(w.all, cta, w.ctas); }
-__device__ __forceinline__ int cta_of(const Walk& w, long long x) {
-    // the last CTA whose range starts at or before x, c < (x + 1) ctas / all (no range is empty:
-    // ctas <= all)
-    const long long a = (x + 1) * w.ctas - 1;
-    return (int)mul_div(a, 1, w.all);
-}
-__device__ __forceinline__ int ctas_of(const ServeParams& p, long long all, int grid) {
-    return (int)min((long long)grid, max(mul_div(all, 1, p.min_blocks), 1ll));
-}
 // the last sequence that starts at or before step x
 __device__ __forceinline__ int seq_at(const ServeParams& p, const long long* pre, long long x) {
     int lo = 0, hi = p.B - 1;
@@ -231,9 +216,7 @@ struct UnitAt {
     Seq s;
     int hg, mt;
     int blk, steps;  // x is its step blk of `steps`
-    int cta0;        // the CTA that begins it
-    int parts;       // CTAs that share it
-    int first_slot;  // where the first one's partials are; piece i > 0 is in slot 2 (cta0 + i)
+    UnitShares by;
 };
 template <int NT, int MODE>
 __device__ __forceinline__ UnitAt unit_at(const ServeParams& p, const long long* pre, const Walk& w, int b, long long x) {
@@ -246,15 +229,8 @@ __device__ __forceinline__ UnitAt unit_at(const ServeParams& p, const long long*
     const int groups = tile_groups<NT>(p, u.s.lq);
     u.hg = unit / groups;
     u.mt = unit - u.hg * groups;
-    u.cta0 = 0;
-    u.parts = 1;
-    u.first_slot = 0;
-    if (!p.whole) {
-        const long long begin = x - u.blk;
-        u.cta0 = cta_of(w, begin);
-        u.parts = cta_of(w, begin + u.steps - 1) - u.cta0 + 1;
-        u.first_slot = 2 * u.cta0 + (range_start(w, u.cta0) == begin ? 0 : 1);
-    }
+    if (p.whole) u.by = {0, 1, 0};
+    else u.by = unit_shares(w.all, w.ctas, x - u.blk, u.steps);
     return u;
 }
 
@@ -268,10 +244,10 @@ __device__ __forceinline__ Walk walk_begin(const ServeParams& p, const long long
         w.x_end = w.all;
     } else {
         w.all = pre[p.B];
-        w.ctas = ctas_of(p, w.all, (int)gridDim.x);
+        w.ctas = range_ctas(w.all, p.min_blocks, (int)gridDim.x);
         if ((int)blockIdx.x < w.ctas && w.all > 0) {
-            w.x = w.x0 = range_start(w, blockIdx.x);
-            w.x_end = range_start(w, blockIdx.x + 1);
+            w.x = w.x0 = range_start(w.all, w.ctas, (int)blockIdx.x);
+            w.x_end = range_start(w.all, w.ctas, (int)blockIdx.x + 1);
             w.b = seq_at(p, pre, w.x);
         }
     }
@@ -308,10 +284,10 @@ __device__ __forceinline__ bool next_seg(Walk& w, Seg<NT>& g, const ServeParams&
         mt = u.mt;
         g.kb_lo = p.whole ? 0 : u.blk;
         hi = p.whole ? 0x7fffffff : u.blk + len;
-        g.parts = u.parts;
-        g.slot = 2 * (int)blockIdx.x + (w.x == w.x0 ? 0 : 1);
+        g.parts = u.by.parts;
+        g.slot = piece_slot((int)blockIdx.x, w.x == w.x0);
         if (w.x == w.x0)
-            w.bound = {g.b, u.hg, u.mt, u.s.q0, u.s.lq, u.cta0, u.blk > 0 ? u.parts : 0, u.first_slot};
+            w.bound = {g.b, u.hg, u.mt, u.s.q0, u.s.lq, u.by.cta0, u.blk > 0 ? u.by.parts : 0, u.by.first_slot};
         w.x += len;
     }
     g.kvh = p.pack ? g.hg : (int)fastdiv((uint32_t)g.hg, p.div_g);
@@ -1620,15 +1596,14 @@ __global__ void __launch_bounds__(kJoinThreads) serve_join_kernel(const __grid_c
     Seq s{};
     s.q0 = u.q0;
     s.lq = u.lq;
-    // of the unit's items, 32 rows x (8 kWide) columns, this boundary's share
-    const int shares = (u.parts - 1) * kJoinBlocks, share = (c - u.cta0 - 1) * kJoinBlocks + (int)blockIdx.y;
-    auto tile_of = [&](int i, int t) { return (i == 0 ? u.first_slot : 2 * (u.cta0 + i)) * NT + t; };
+    auto tile_of = [&](int i, int t) { return part_slot(u.cta0, u.first_slot, i) * NT + t; };
     auto lse_of = [&](int i, int t, int row) { return __ldcg(p.part_lse + (size_t)tile_of(i, t) * 128 + row); };
     auto join = [&](auto wide_c, auto ahead_c) {
         constexpr int kWide = decltype(wide_c)::value, kAhead = decltype(ahead_c)::value;
         constexpr int kCols = HD / (8 * kWide), kItems = NT * 4 * kCols;
-        const int end = kItems * (share + 1) / shares;
-        for (int item = kItems * share / shares + (threadIdx.x >> 5); item < end; item += kJoinThreads / 32) {
+        // of the unit's items, 32 rows x (8 kWide) columns, this boundary's share
+        const JoinShare mine = join_share(kItems, c, u.cta0, u.parts, (int)blockIdx.y, kJoinBlocks);
+        for (int item = mine.lo + (threadIdx.x >> 5); item < mine.hi; item += kJoinThreads / 32) {
             const int col = item % kCols, t = item / kCols / 4, row = item / kCols % 4 * 32 + lane;
             const RowMap rm = row_map(p, s.lq, (u.mt * NT + t) * p.pos_per_tile, u.hg, row);
             if (!rm.ok) continue;

@@ -20,7 +20,7 @@ struct ServeBound {
     int q0, lq;      // its sequence's first query row and queries
     int cta0;        // the CTA that begins it
     int parts;       // CTAs that share it
-    int first_slot;  // where the first one's partials are; piece i > 0 is in slot 2 (cta0 + i)
+    int first_slot;  // where the first one's partials are
 };
 
 struct ServeParams {
