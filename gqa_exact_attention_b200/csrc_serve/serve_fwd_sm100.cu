@@ -34,6 +34,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "exp2_poly4.cuh"
 #include "launch_serve.h"
 #include "ptx_sm100.cuh"
 #include "serve_params.h"
@@ -107,28 +108,6 @@ struct Cfg {
     }
     static constexpr int kPAfterO = NT * HD;  // separate P lies this many columns past O
 };
-
-// 2^x on two lanes at once on the FMA pipe: x = j + f with j the nearest integer, 2^f by the
-// degree-4 polynomial with constant term 1 that has the least relative error on [-1/2, 1/2]
-// (2.8e-6: below the sums' and far below bf16's rounding), and j added to the exponent.  x is at
-// most 8 here; below -126 it counts as -126.
-__device__ __forceinline__ void exp2_poly4(float x0, float x1, float& y0, float& y1) {
-    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it leaves j in the low bits
-    constexpr float c1 = 0.6931241750717163f, c2 = 0.24024099111557007f, c3 = 0.055906426161527634f,
-                    c4 = 0.009582853876054287f;
-    x0 = fmaxf(x0, -126.f);
-    x1 = fmaxf(x1, -126.f);
-    float t0, t1, r0, r1, f0, f1, q0, q1;
-    add2(x0, x1, kRound, kRound, t0, t1);
-    add2(t0, t1, -kRound, -kRound, r0, r1);
-    add2(x0, x1, -r0, -r1, f0, f1);
-    fma2(f0, f1, c4, c4, c3, c3, q0, q1);
-    fma2(q0, q1, f0, f1, c2, c2, q0, q1);
-    fma2(q0, q1, f0, f1, c1, c1, q0, q1);
-    fma2(q0, q1, f0, f1, 1.f, 1.f, q0, q1);
-    y0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-    y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
-}
 
 template <uint32_t R>
 __device__ __forceinline__ void regs_inc() {
