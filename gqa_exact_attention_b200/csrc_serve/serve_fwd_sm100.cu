@@ -11,8 +11,10 @@
 //  - LIST (many tiles: prompts): a sorted list of tile groups, whole units, dealt over the
 //    CTAs in alternating direction; bound by the tensor pipe.
 //  - ranges (few rows over many keys: trees, short prompts): all units' key blocks in one
-//    row, cut into one equal range per CTA.  Every CTA streams the same number of blocks
-//    whatever the lengths are; a unit that several CTAs share leaves fp32 partials, which a
+//    row, cut into one equal range per CTA.  Without a causal mask every CTA streams the same
+//    number of blocks whatever the lengths are.  A causal unit counts all key blocks of its
+//    sequence, those past its diagonal too, so CTAs at a prompt's early tiles have less to do
+//    than those at its late ones.  A unit that several CTAs share leaves fp32 partials, which a
 //    second kernel joins in the order of the keys.  Bound by HBM.
 // Roles:
 //   warpgroup 0, warp 0   TMA producer: Q tiles once per unit, then a ring of K/V blocks.
@@ -24,11 +26,12 @@
 //   warpgroup NT + 1      (NT = 2 only) epilogue.  With NT = 1 the softmax warpgroup writes.
 // NT = 2: one CTA per SM.  NT = 1: two, so that one's unit changes overlap the other's stream.
 //
-// Measured on B200: 64 causal prompts of 1024 to 2048 tokens (Hq 32, Hk 8, d 128) 1.64 ms, 800
-// TFLOP/s under the power cap (tensor pipe 53 %, exponentials 51 % busy: the chain S, softmax, P V
-// of two tiles is latency; 64-key halves of S, dynamic units and programmatic launches were all
-// slower); 64 sequences of up to 16384 keys with 16 drafted tokens 0.52 ms from pages of 16, 5.5
-// TB/s, 0.45 ms from pages of 64, 6.2 TB/s; one sequence of 8192 keys 28 us.
+// Measured on B200 (several boxes): 64 causal prompts of 1024 to 2048 tokens (Hq 32, Hk 8, d 128)
+// 1.64-1.71 ms, 770-800 TFLOP/s under the power cap (tensor pipe and exponentials each about half
+// busy: the chain S, softmax, P V of two tiles is latency; 64-key halves of S, dynamic units and
+// programmatic launches were all slower); 64 sequences of up to 16384 keys with 16 drafted tokens
+// 0.52-0.62 ms from pages of 16, 4.6-5.5 TB/s, 0.45 ms from pages of 64, 6.2 TB/s; one sequence of
+// 8192 keys 28 us; one causal prompt of 2048 in ranges (Hq 8, Hk 2, d 64) 36 us.
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
