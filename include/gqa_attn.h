@@ -26,9 +26,9 @@
  *    out = 0 and lse = -inf.
  *  - Scores that are not finite: a row that sees a key whose s_j is NaN or +inf gets NaN in
  *    out and lse; one of -inf weighs nothing, and a row all of whose scores are -inf is one
- *    with no allowed key.  (With scale = 0 a product q.k of -inf may count as 0 or as NaN.)
- *    A value of v that is not finite reaches every row of its 128-key
- *    block.
+ *    with no allowed key.  (With scale = 0, a product q.k of -inf leaves its
+ *    row's values unspecified.)  A value of v that is not finite reaches every row of its
+ *    128-key block.
  *
  * Scheduling variants (results do not depend on them beyond fp32 rounding order):
  *  - pack_gqa: the Hq/Hk query heads of one kv group are folded into the rows of one

@@ -43,7 +43,7 @@ extern "C" {
  * What other sequences hold does not reach a sequence's result, not even infinities or NaN.
  * Within a sequence, a row that sees a key whose score is NaN or +inf gets NaN in out and lse; a
  * score of -inf weighs nothing, and a row all of whose scores are -inf is one that sees no key.
- * (With scale = 0 a product q.k of -inf may count as 0 or as NaN.)
+ * (With scale = 0, a product q.k of -inf leaves its row's values unspecified.)
  * A value of V that is not finite reaches every row of its 128-key block, as in gqa_attn_fwd.
  *
  * total_q = 0 returns GQA_OK and does nothing; total_k = 0 is a batch without keys (k and v
